@@ -24,6 +24,9 @@ __all__ = [
     "from_slots_one_launch", "apply_linear_from_experts_", "from_experts_one_launch", "apply_",
     "Backend",
     "workspace_bytes", "STATUS", "column_linear", "fused_column_linear",
+    "MXFP4", "Routing", "ExpertRows", "route_experts", "expert_rows", "combine_experts",
+    "quantize_mxfp4", "gather_quantize_mxfp4", "silu_mul_quantize_mxfp4", "dequantize_mxfp4",
+    "mxfp4_linear", "mxfp4_expert_linear",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +82,20 @@ SIGNATURES = {
     "lora_fused_column_linear": (ctypes.c_int, [ctypes.c_int, _P, _P, _P, _I64, _I64, _P, _I32,
                                                 _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
     "lora_fused_column_linear_workspace_bytes": (_SZ, [_I64, _I64, _I32, _I32]),
+    "lora_route_experts": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I32, _I32, _I32, _P, _I32,
+                                          _I32, _I32, _I32, ctypes.c_float, _P, _P, _P]),
+    "lora_expert_rows": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "lora_expert_rows_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "lora_combine_experts": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _P, _P, _I64, _I32, _P,
+                                            _P, _P]),
+    "lora_mxfp4_scale_row_bytes": (_I64, [_I64]),
+    "lora_quantize_mxfp4": (ctypes.c_int, [ctypes.c_int, _I32, _P, _I64, _P, _I64, _I64, _P, _P,
+                                           _P, _P]),
+    "lora_dequantize_mxfp4": (ctypes.c_int, [ctypes.c_int, _P, _P, _I64, _I64, _P, _P]),
+    "lora_mxfp4_linear": (ctypes.c_int, [ctypes.c_int, _P, _P, _I64, _P, _P, _I64, _I64, _P,
+                                         _P]),
+    "lora_mxfp4_expert_linear": (ctypes.c_int, [ctypes.c_int, _P, _P, _I64, _P, _P, _I64, _I64,
+                                                _P, _I32, _P, _P]),
 }
 
 
@@ -494,3 +511,9 @@ class Backend:
 
     def apply_(self, x, y, a, b, addressing, ranks, scalings, out_slices, embedding=False):
         return apply_(x, y, a, b, addressing, ranks, scalings, out_slices, embedding)
+
+
+from .experts import (  # noqa: E402  (the routed-expert operators use the helpers above)
+    MXFP4, ExpertRows, Routing, combine_experts, dequantize_mxfp4, expert_rows,
+    gather_quantize_mxfp4, mxfp4_expert_linear, mxfp4_linear, quantize_mxfp4, route_experts,
+    silu_mul_quantize_mxfp4)

@@ -22,7 +22,9 @@ LIB_NAME = "liblora_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["addressing.hip", "gather_shrink.hip", "shrink.hip", "expand.hip", "fused.hip",
-           "sgmv.hip", "linear_lora.hip", "noalloc.hip", "lora_api.cpp"]
+           "sgmv.hip", "linear_lora.hip", "noalloc.hip", "lora_api.cpp",
+           "experts/route.hip", "experts/expert_rows.hip", "experts/mxfp4.hip",
+           "experts/mxfp4_linear.hip", "experts/experts_api.cpp"]
 
 ARCH = "gfx950"
 # Packed fp32 VALU ops are kept off: the compiler must not form v_pk_* fp32
@@ -45,7 +47,7 @@ def hipcc() -> str:
 
 
 def _compile(src: str) -> str:
-    obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+    obj = os.path.join(BUILD, os.path.splitext(src)[0].replace("/", "_") + ".o")
     cmd = [hipcc(), *COMMON, *DEVICE_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"

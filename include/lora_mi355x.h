@@ -435,6 +435,129 @@ lora_status lora_apply_linear_noalloc(int dtype, const void* x, void* y, int64_t
 /* Size in bytes of lora_apply_linear_noalloc's static scratch array. */
 size_t lora_noalloc_scratch_bytes(void);
 
+/* ------------------------------------------------------------------------
+ * Routed experts: the operators around the experts' LoRA.
+ *
+ *   lora_route_experts        logits -> each token's experts and weights
+ *   lora_expert_rows          the (token, choice) pairs sorted by expert
+ *   lora_quantize_mxfp4       rows -> MXFP4 (also gathered, or silu(gate) * up)
+ *   lora_dequantize_mxfp4     MXFP4 -> rows
+ *   lora_mxfp4_linear         x @ W^T, both in MXFP4
+ *   lora_mxfp4_expert_linear  the same with each row's expert's weight
+ *   lora_combine_experts      the experts' rows weighted and summed per token
+ *
+ * The conventions above hold. Limits checked on the host: 1 <= num_experts
+ * <= 1024, 1 <= top_k <= 32, T * top_k < 2^31, rows < 2^31, N and K at most
+ * 2^20.
+ *
+ * MXFP4 of rows of K values (K a multiple of 32):
+ *   codes  [rows, K / 2]  uint8: two 4-bit codes a byte, the even element low.
+ *                         A code is a sign (bit 3) and one of 0, 0.5, 1, 1.5,
+ *                         2, 3, 4, 6 (bits 2:0)
+ *   scales [rows, ld]     uint8, ld = K / 32 rounded up to a multiple of 4
+ *                         (lora_mxfp4_scale_row_bytes): one byte b per 32
+ *                         values, 2^(b - 127); 255 is not a number. Padding
+ *                         bytes are written as 0 and never read as scales.
+ * codes are 16-byte aligned, scales 4-byte aligned.
+ */
+enum { LORA_SCORES_SOFTMAX = 0, LORA_SCORES_SIGMOID = 1 };
+enum { LORA_GROUP_MAX = 0, LORA_GROUP_SUM2 = 1 };
+enum { LORA_QUANTIZE_PLAIN = 0, LORA_QUANTIZE_GATHER = 1, LORA_QUANTIZE_SILU_MUL = 2 };
+
+/*
+ * lora_route_experts: for each token t of logits [T, num_experts] (dtype), in
+ * float32: s = softmax(logits[t]) or sigmoid(logits[t]) (scores), c = s + bias
+ * (float32 [num_experts], NULL: none). With top_groups < groups the experts
+ * form `groups` groups of consecutive ones; a group is worth its best c
+ * (LORA_GROUP_MAX) or the sum of its two best (LORA_GROUP_SUM2), and only the
+ * top_groups best groups stay. ids [T, top_k] receives the experts of the
+ * top_k largest c, largest first; weights [T, top_k] their s, divided by
+ * their sum where renormalize is not 0 (0 where that sum is 0), times scaling.
+ * Equal values go to the lowest expert or group. An expert whose logit or c
+ * is NaN or -inf is not available (a logit of +inf counts as the largest
+ * finite float); where fewer than top_k are left, the remaining ids are -1
+ * and their weights 0. groups is at most 16 and divides num_experts.
+ * T = 1 and any T alike take one launch.
+ */
+lora_status lora_route_experts(int dtype, const void* logits, int64_t T, int32_t num_experts,
+                               int32_t top_k, int32_t scores, const float* bias, int32_t groups,
+                               int32_t top_groups, int32_t group_score, int32_t renormalize,
+                               float scaling, int32_t* ids, float* weights, void* stream);
+
+/*
+ * lora_expert_rows: sorts the choices of ids [T, top_k] by expert, stably (a
+ * row per choice, in ascending token and choice within an expert). A choice
+ * outside [0, num_experts) is dead: its row comes after every expert's.
+ *   row_token [T * top_k]     the token of each row
+ *   positions [T, top_k]      the row of each choice, -1 for a dead one
+ *   offsets   [num_experts+1] expert e owns rows [offsets[e], offsets[e+1])
+ *   row_slot  [T * top_k]     token_slot of each row's token, -1 for a dead
+ *                             row (NULL exactly where token_slot is NULL)
+ * offsets and row_slot are what lora_build_addressing_experts and
+ * lora_apply_linear_from_experts take. The workspace (contents need no
+ * initialisation) holds lora_expert_rows_workspace_bytes.
+ */
+lora_status lora_expert_rows(const int32_t* ids, int64_t T, int32_t top_k, int32_t num_experts,
+                             const int32_t* token_slot, int32_t* row_token, int32_t* positions,
+                             int32_t* offsets, int32_t* row_slot, void* workspace,
+                             size_t workspace_bytes, void* stream);
+size_t lora_expert_rows_workspace_bytes(int64_t T, int32_t top_k, int32_t num_experts);
+
+/*
+ * lora_combine_experts: y[t] = residual[t] + sum over j of weights[t, j] *
+ * rows[positions[t, j]], formed in float32 and rounded once to dtype. rows
+ * [num_rows, width], residual (NULL: none) and y [T, width] are of dtype;
+ * residual may be y. A position outside [0, num_rows) adds nothing, and its
+ * weight is not read.
+ */
+lora_status lora_combine_experts(int dtype, const void* rows, int64_t num_rows, int64_t width,
+                                 const int32_t* positions, const float* weights, int64_t T,
+                                 int32_t top_k, const void* residual, void* y, void* stream);
+
+/* Bytes of one scale row of K values (0 on bad input). */
+int64_t lora_mxfp4_scale_row_bytes(int64_t K);
+
+/*
+ * lora_quantize_mxfp4: per block of 32 values, b = clamp(floor(log2(max |v|))
+ * - 2 + 127, 0, 254) (0 for an all-zero block; 255, with codes 0, where a
+ * value is NaN or infinite), and codes nearest to v * 2^(127 - b), ties to
+ * the even code, values past 6 at 6.
+ *   LORA_QUANTIZE_PLAIN     v = x[r], x [x_rows >= rows, K]
+ *   LORA_QUANTIZE_GATHER    v = x[row_index[r]] (clamped to [0, x_rows)),
+ *                           also copied to rows_out [rows, K]
+ *   LORA_QUANTIZE_SILU_MUL  x [x_rows >= rows, 2 K] holds gate and up; v =
+ *                           silu(gate) * up, formed in float32 and rounded to
+ *                           dtype, also stored to rows_out [rows, K]
+ */
+lora_status lora_quantize_mxfp4(int dtype, int32_t form, const void* x, int64_t x_rows,
+                                const int32_t* row_index, int64_t rows, int64_t K, void* rows_out,
+                                uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values that codes and scales stand for, in out [rows, K] (dtype). */
+lora_status lora_dequantize_mxfp4(int dtype, const uint8_t* codes, const uint8_t* scales,
+                                  int64_t rows, int64_t K, void* out, void* stream);
+
+/*
+ * lora_mxfp4_linear: y [rows, N] = x @ W^T with x [rows, K] and W [N, K] in
+ * MXFP4, accumulated in float32 and rounded once to dtype. The LoRA delta of
+ * a target goes onto y with lora_apply_linear.
+ */
+lora_status lora_mxfp4_linear(int dtype, const uint8_t* x_codes, const uint8_t* x_scales,
+                              int64_t rows, const uint8_t* w_codes, const uint8_t* w_scales,
+                              int64_t N, int64_t K, void* y, void* stream);
+
+/*
+ * lora_mxfp4_expert_linear: the same over expert-sorted rows: row r of expert
+ * e (offsets[e] <= r < offsets[e+1]) meets the weight W[e] of W
+ * [num_experts, N, K]. Rows outside [offsets[0], offsets[num_experts]) are
+ * set to 0. An expert with no rows costs nothing.
+ */
+lora_status lora_mxfp4_expert_linear(int dtype, const uint8_t* x_codes, const uint8_t* x_scales,
+                                     int64_t rows, const uint8_t* w_codes,
+                                     const uint8_t* w_scales, int64_t N, int64_t K,
+                                     const int32_t* offsets, int32_t num_experts, void* y,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif
