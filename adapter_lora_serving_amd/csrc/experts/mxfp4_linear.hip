@@ -12,6 +12,8 @@
 // rows are operand A and the x rows operand B, so a lane ends with 4
 // consecutive columns of one row of y. Products of two 4-bit values and the
 // powers of two are exact; the sums are fp32, y is rounded once.
+#include <algorithm>
+#include <type_traits>
 #include "lora_common.h"
 #include "experts.h"
 
@@ -20,120 +22,514 @@ namespace lora {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes from any element on
 
-__device__ __forceinline__ f32x4 mfma_mx(u32x4 a, u32x4 b, f32x4 c, int sa, int sb) {
+// D[32x32] += A[32 x 64] . B[32 x 64]^T: lane (m = lane & 31, h = lane >> 5)
+// supplies row m, one block of 32 codes, and byte J of its scale word as that
+// block's scale; it receives D[8 (i / 4) + 4 h + i % 4][m] in element i.
+template <int J>
+__device__ __forceinline__ f32x16 mfma_mx32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb) {
   const i32x8 A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const i32x8 B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, sa, 0, sb);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, J, (int)sa, J, (int)sb);
 }
 
-// Segment s of the rows: 0 is the rows before the first expert, 1 .. E the
-// experts, E + 1 the rows after the last. Clamped, so malformed offsets give
-// wrong values but no access outside the buffers.
-__device__ __forceinline__ void segment_rows(const int32_t* __restrict__ offs, int s, int E,
-                                             int rows, int& beg, int& n) {
-  const int b = s == 0 ? 0 : min(max(offs[s - 1], 0), rows);
-  const int e = s == E + 1 ? rows : min(max(offs[s], b), rows);
-  beg = b;
-  n = max(e - b, 0);
+constexpr int kStageK = 256;        // K of one LDS stage
+constexpr int kRowB = kStageK / 2;  // code bytes of a row in it
+// an operand tile is at most 2^27 bytes, so an offset past kPastEnd, with or
+// without kOOB, is outside it
+constexpr uint32_t kPastEnd = 0x40000000u;
+
+// One 4-byte global -> LDS transfer per lane: lane L to byte 4 L of dst.
+__device__ __forceinline__ void dma4(rsrc_t r, char* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, (int)off, 0, 0, 0);
+}
+
+// scale bytes of blocks [b, b + 4) of a row with kb blocks, the rest cleared
+__device__ __forceinline__ uint32_t keep_blocks(uint32_t v, int b, int kb) {
+  const int n = kb - b;
+  return n >= 4 ? v : n <= 0 ? 0u : v & ((1u << (8 * n)) - 1u);
+}
+
+// s_waitcnt operand: at most n vector memory operations and no LDS operation
+// outstanding; 63 vector memory operations are not waited for at all.
+constexpr int vm_lds(int n) { return vmcnt_le(n) & ~(15 << 8); }
+
+// Workgroup barrier that waits for the wave's LDS operations alone, so that
+// transfers and stores stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(vm_lds(63));
+  barrier_no_fence();
+}
+
+// Compute units of the current device.
+hipError_t compute_units(int* n) {
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  return e != hipSuccess
+             ? e
+             : hipDeviceGetAttribute(n, hipDeviceAttributeMultiprocessorCount, dev);
 }
 
 }  // namespace
 
-// 64 x 64 tile of y, 4 waves of 32 x 32, operands straight from memory.
+// Rows of y outside [offsets[0], offsets[E]), by the whole grid.
 template <typename D>
-__global__ __launch_bounds__(256) void k_mx_simple(MxArgs a, int sld) {
-  __shared__ int scratch[24];
+__device__ __forceinline__ void zero_dead_rows(const MxArgs& a) {
+  const int lo = min(max(a.offsets[0], 0), a.rows);
+  const int hi = min(max(a.offsets[a.E], lo), a.rows);
+  const int64_t dead = (int64_t)(lo + a.rows - hi) * a.N;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < dead;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t at = i < (int64_t)lo * a.N ? i : i + (int64_t)(hi - lo) * a.N;
+    if constexpr (D::kBytes == 2) ((uint16_t*)a.y)[at] = 0; else ((float*)a.y)[at] = 0.0f;
+  }
+}
+
+// LDS of a tile kernel (stages, scale slots, scratch), and the workgroups of
+// it that a compute unit's 160 KB hold (at most 16 waves of them: with more,
+// fewer registers a wave than its accumulators and operands need)
+template <int BM, int BN, int NW, int NST, bool SCREG>
+constexpr int lds_bytes() {
+  constexpr int SRowB = SCREG ? 16 : 8;
+  return NST * ((BM + BN) * kRowB + ((BM + BN) * SRowB / 256 + NW - 1) / NW * NW * 256) + 128;
+}
+template <int BM, int BN, int NW, int NST, bool SCREG>
+constexpr int occupancy() {
+  constexpr int by_lds = 163840 / lds_bytes<BM, BN, NW, NST, SCREG>();
+  return by_lds * NW > 16 ? 16 / NW : by_lds;
+}
+
+// BM x BN tiles of y, by a workgroup of WM x WN waves that walks its share of
+// them. K passes in stages of 256 through a ring of NST LDS stages; the ring
+// runs on from one tile into the next, so a tile's first stage is on its way
+// while the tile before it is finished and stored.
+template <typename D, int BM, int BN, int WM, int WN, int NST, bool SCREG>
+__global__ __launch_bounds__(64 * WM * WN, (occupancy<BM, BN, WM * WN, NST, SCREG>() * WM * WN / 4)) void
+k_mx_tile(MxArgs a, int sld, int ntiles) {
+  static_assert(!SCREG || NST == 2, "scale registers look one stage ahead");
+  static_assert(WM * WN % 2 == 0, "the swizzle of a wave's transfers is the same for all of them");
+  constexpr int NW = WM * WN;
+  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+  constexpr int RPI = 8;                                    // rows of a transfer
+  constexpr int kStageB = (BM + BN) * kRowB;
+  constexpr int XI = BM / RPI / NW, WI = BN / RPI / NW;     // transfers a wave and stage
+  // scales: by way of registers in chunks of two stages, 16 bytes a row; else
+  // by transfers with their stage, 8 bytes a row
+  constexpr int SRowB = SCREG ? 16 : 8;
+  constexpr int SRows = 256 / SRowB;                        // rows of a scale transfer
+  constexpr int SI = ((BM + BN) * SRowB / 256 + NW - 1) / NW;
+  constexpr int kScaleB = SI * NW * 256;                    // scale bytes of a slot
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* lsc = lds + NST * kStageB;
+  int* scratch = (int*)(lsc + NST * kScaleB);
+  const int tid = threadIdx.x;
   const int lane = lane_id();
   const int w = wave_id();
-  const int m = lane & 15, g = lane >> 4;
-  int beg = 0, n = a.rows, e = 0, tile = blockIdx.y;
-  bool zero = false;
-  if (a.offsets) {
-    const SlotItem it = locate_item(
-        (int)blockIdx.y, a.E + 2,
-        [&](int s) {
-          int b, c;
-          segment_rows(a.offsets, s, a.E, a.rows, b, c);
-          return (c + 63) / 64;
-        },
-        scratch);
-    if (it.slot < 0) return;
-    segment_rows(a.offsets, it.slot, a.E, a.rows, beg, n);
-    e = it.slot - 1;
-    zero = e < 0 || e >= a.E;
-    if (zero) e = 0;
-    tile = it.local;
-  }
-  const int r0 = tile * 64 + (w & 1) * 32;         // within the segment
-  const int c0 = blockIdx.x * 64 + (w >> 1) * 32;
+  const uint32_t rowb = (uint32_t)a.K / 2;
   const int kb = a.K / 32;
-  const int64_t rowb = a.K / 2;
-  const uint8_t* W = a.w + (int64_t)e * a.N * rowb;
-  const uint8_t* WS = a.ws + (int64_t)e * a.N * sld;
-  f32x4 acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (!zero) {
-    for (int b0 = 0; b0 < kb; b0 += 4) {
-      const int b = b0 + g;
-      u32x4 xo[2], wo[2];
-      int xsc[2], wsc[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = r0 + i * 16 + m, c = c0 + i * 16 + m;
-        xo[i] = wo[i] = u32x4{0u, 0u, 0u, 0u};
-        xsc[i] = wsc[i] = 0;
-        if (b < kb && r < n) {
-          xo[i] = *(const u32x4*)(a.x + (int64_t)(beg + r) * rowb + b * 16);
-          xsc[i] = a.xs[(int64_t)(beg + r) * sld + b];
-        }
-        if (b < kb && c < a.N) {
-          wo[i] = *(const u32x4*)(W + (int64_t)c * rowb + b * 16);
-          wsc[i] = WS[(int64_t)c * sld + b];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_mx(wo[i], xo[j], acc[i][j], wsc[i], xsc[j]);
-    }
+  const int kt = (a.K + kStageK - 1) / kStageK;   // at least NST - 1
+
+  // the experts' row tiles; rows of no expert become zero
+  int mtiles = (a.rows + BM - 1) / BM;
+  SlotScan sc;
+  auto info = [&](int s, int* v) {
+    segment_of(a.offsets, s, a.rows, v[0], v[1]);
+    v[2] = 0;
+  };
+  auto count = [&](const int* v) { return (v[1] + BM - 1) / BM; };
+  if (a.offsets) {
+    sc = scan_slots(a.E, info, count, scratch);
+    mtiles = sc.total;
+    zero_dead_rows<D>(a);
   }
-  // wait states between the last MFMA and the first vector read of its result
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
+
+  // block b runs on XCD b % 8, which takes a run of positions of an order in
+  // which 8 row tiles vary fastest, so that the tiles an XCD runs at a time
+  // share their operands in its L2
+  const int G = mtiles * ntiles;
+  const int per = (G + 7) / 8;
+  const int stride = (int)gridDim.x >> 3;
+  const int end = min(G - ((int)blockIdx.x & 7) * per, per);   // positions of this XCD
+  int pos = (int)blockIdx.x >> 3;
+  if (pos >= end) return;
+  struct Tile {
+    int row, mrows, n0, ncols, e;   // first row of y, rows, first column, columns, expert
+  };
+  auto locate = [&](int p) {
+    constexpr int kGroupM = 8;
+    const int L = ((int)blockIdx.x & 7) * per + p;
+    const int grp = L / (kGroupM * ntiles);
+    const int gsz = min(kGroupM, mtiles - grp * kGroupM);
+    const int li = L - grp * kGroupM * ntiles;
+    const int tm = grp * kGroupM + li % gsz;
+    Tile t;
+    t.n0 = li / gsz * BN;
+    t.ncols = min(BN, a.N - t.n0);
+    t.e = 0;
+    t.row = tm * BM;
+    t.mrows = min(BM, a.rows - t.row);
+    if (a.offsets) {
+      SlotItem it;
+      int v[3];
+      __syncthreads();   // scratch is free again
+      pick_item(sc, tm, info, count, scratch, it, v);
+      t.e = it.slot;
+      t.row = v[0] + it.local * BM;
+      t.mrows = min(BM, v[1] - it.local * BM);
+    }
+    return t;
+  };
+
+  // operand and scale buffers of a tile
+  rsrc_t x_r, w_r;
+  auto xs_of = [&](const Tile& t) {
+    return make_rsrc(a.xs + (int64_t)t.row * sld, (uint32_t)(t.mrows * sld));
+  };
+  auto ws_of = [&](const Tile& t) {
+    return make_rsrc(a.ws + ((int64_t)t.e * a.N + t.n0) * sld, (uint32_t)(t.ncols * sld));
+  };
+  // global -> LDS without registers: an instruction of a wave fills 8 rows of
+  // 128 bytes, lane L at row L / 8, physical chunk L % 8 of 16 bytes; the
+  // lane fetches the logical chunk stored there, L % 8 ^ (row / 2) % 8, so
+  // that the operand reads of 16 consecutive rows spread over the banks
+  // (with row % 8 in its place rows r and r + 8 meet: 366 us against 318 us
+  // for the products and reads of a 8192 x 28672 x 4096 product)
+  const int pr = lane >> 3;
+  auto swz = [](int row) { return row >> 1 & 7; };
+  const uint32_t pc = (uint32_t)((lane & 7) ^ swz(w * RPI + pr)) * 16u;
+  uint32_t xoff[XI], woff[WI], soff[SCREG ? 1 : SI];
+  rsrc_t xs_r, ws_r;
+  auto point_at = [&](const Tile& t) {
+    x_r = make_rsrc(a.x + (int64_t)t.row * rowb, (uint32_t)t.mrows * rowb);
+    w_r = make_rsrc(a.w + ((int64_t)t.e * a.N + t.n0) * rowb, (uint32_t)t.ncols * rowb);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < XI; ++i) {
+      const int row = (w + NW * i) * RPI + pr;
+      xoff[i] = row < t.mrows ? (uint32_t)row * rowb + pc : kOOB;
+    }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int i = 0; i < WI; ++i) {
+      const int row = (w + NW * i) * RPI + pr;
+      woff[i] = row < t.ncols ? (uint32_t)row * rowb + pc : kOOB;
+    }
+    if constexpr (!SCREG) {
+      xs_r = xs_of(t);
+      ws_r = ws_of(t);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = r0 + j * 16 + m, c = c0 + i * 16 + 4 * g + q;
-        if (r < n && c < a.N) {
-          const int64_t at = (int64_t)(beg + r) * a.N + c;
-          if constexpr (D::kBytes == 2)
-            ((uint16_t*)a.y)[at] = (uint16_t)to_bf16_bits(acc[i][j][q]);
-          else
-            ((float*)a.y)[at] = acc[i][j][q];
+      for (int i = 0; i < SI; ++i) {
+        const int row = (w + NW * i) * SRows + (lane >> 1);
+        const int rr = row < BM ? row : row - BM;
+        soff[i] = rr < (row < BM ? t.mrows : row < BM + BN ? t.ncols : 0)
+                      ? (uint32_t)rr * sld + (lane & 1) * 4 : kOOB;
+      }
+    }
+  };
+  auto issue = [&](int it, int slot) {
+    const uint32_t k0 = (uint32_t)it * kRowB;
+    const uint32_t ko = k0 + pc < rowb ? k0 : kPastEnd;
+    char* sb = lds + slot * kStageB;
+#pragma unroll
+    for (int i = 0; i < XI; ++i) dma16(x_r, sb + (w + NW * i) * 1024, xoff[i] + ko);
+#pragma unroll
+    for (int i = 0; i < WI; ++i)
+      dma16(w_r, sb + BM * kRowB + (w + NW * i) * 1024, woff[i] + ko);
+    if constexpr (!SCREG) {
+      const uint32_t b0 = (uint32_t)it * 8;
+      const uint32_t so = b0 + (lane & 1) * 4 < (uint32_t)sld ? b0 : kPastEnd;
+#pragma unroll
+      for (int i = 0; i < SI; ++i)
+        dma4((w + NW * i) * SRows < BM ? xs_r : ws_r, lsc + slot * kScaleB + (w + NW * i) * 256,
+             soff[i] + so);
+    }
+  };
+
+  // Scales by way of registers: a group is 64 bytes (K of 2048) of every row,
+  // read by 4 lanes side by side so that a line is asked for once, and handed
+  // to LDS a chunk at a time by the lanes that hold it. The same bytes by
+  // stage-wise transfers would ask L2 for every line many times.
+  const int piece = lane & 3;
+  u32x4 sreg[SCREG ? SI : 1];
+  auto load_scales = [&](const Tile& t, int grp) {
+    const int b = grp * 64 + piece * 16;
+    // 16 bytes that would run past the row (sld >= 16) end with it instead
+    const uint32_t o = b < sld ? (uint32_t)min(b, sld - 16) : kPastEnd;
+    const rsrc_t xr = xs_of(t), wr = ws_of(t);
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+      const int first = (w + NW * i) * 16;   // the 16 rows are all of x or all of W
+      const int rr = first + (lane >> 2) - (first < BM ? 0 : BM);
+      const int lim = first < BM ? t.mrows : first < BM + BN ? t.ncols : 0;
+      sreg[i] = bload16(first < BM ? xr : wr, (rr < lim ? (uint32_t)rr * sld : kOOB) + o);
+    }
+  };
+  auto store_scales = [&](int chunk, int slot) {
+    char* cb = lsc + slot * kScaleB + (lane >> 2) * 16;
+    const int back = max(chunk * 16 + 16 - sld, 0);   // bytes that load_scales moved back
+    if (piece == (chunk & 3)) {
+#pragma unroll
+      for (int i = 0; i < SI; ++i) {
+        u32x4 v = sreg[i];
+        if (back > 0)
+          v = back == 4 ? u32x4{v.y, v.z, v.w, 0u}
+              : back == 8 ? u32x4{v.z, v.w, 0u, 0u} : u32x4{v.w, 0u, 0u, 0u};
+        *(u32x4*)(cb + (w + NW * i) * 256) = v;
+      }
+    }
+  };
+
+  // cur: the tile being multiplied; ld: the tile being fetched, stage lit
+  // next; nx: the one after it (its scales are fetched ahead of it)
+  Tile cur = locate(pos), ld = cur, nx = cur;
+  pos += stride;
+  bool has_ld = true, has_nx = pos < end;
+  if (has_nx) nx = locate(pos);
+  int lit = 0, lslot = 0, chunks = 0;
+  point_at(ld);
+  if constexpr (SCREG) load_scales(ld, 0);
+  // fetch the next stage of the walk, if there is one
+  auto fetch = [&]() {
+    if (lit == kt) {
+      lit = 0;
+      has_ld = has_nx;
+      if (has_nx) {
+        ld = nx;
+        pos += stride;
+        has_nx = pos < end;
+        if (has_nx) nx = locate(pos);
+        point_at(ld);
+      }
+    }
+    if (!has_ld) return;
+    if constexpr (SCREG) {
+      // before the transfers, which a wait for the registers would wait for too
+      if (lit % 2 == 0) {
+        const int c = lit / 2;
+        store_scales(c, chunks++ & 1);
+        if (lit + 2 >= kt) {
+          if (has_nx) load_scales(nx, 0);
+        } else if (c % 4 == 3) {
+          load_scales(ld, c / 4 + 1);
         }
       }
+    }
+    issue(lit, lslot);
+    lslot = lslot + 1 == NST ? 0 : lslot + 1;
+    ++lit;
+  };
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) fetch();
+
+  const int m = lane & 31, h = lane >> 5;
+  const int wm = w % WM, wn = w / WM;
+  const uint32_t sw = (uint32_t)(((4 * h) ^ swz(m)) << 4);   // chunk of step 0
+  const uint32_t xrow = (uint32_t)(wm * TM * 32 + m) * kRowB;
+  const uint32_t wrow = (uint32_t)(BM + wn * TN * 32 + m) * kRowB;
+  const uint32_t xsc = (uint32_t)(wm * TM * 32 + m) * SRowB + 4 * h;
+  const uint32_t wsc = (uint32_t)(BM + wn * TN * 32 + m) * SRowB + 4 * h;
+
+  int slot = 0, cslot = 1;
+  for (;;) {
+    f32x16 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+
+    for (int it = 0; it < kt; ++it) {
+      // this stage is there once at most the transfers of the later ones are
+      // outstanding; then the barrier makes every wave's part visible and
+      // frees the buffer read in the previous iteration
+      constexpr int AH = NST - 2, OPS = XI + WI + SI;
+      if (AH > 0 && has_ld)
+        __builtin_amdgcn_s_waitcnt(vm_lds(AH * OPS));
+      else
+        __builtin_amdgcn_s_waitcnt(vm_lds(0));
+      barrier_no_fence();
+      fetch();
+      if (SCREG && it % 2 == 0) cslot ^= 1;
+      const char* sb = lds + slot * kStageB;
+      const char* ss = SCREG ? lsc + cslot * kScaleB + it % 2 * 8 : lsc + slot * kScaleB;
+      uint32_t sx[TM], sv[TN];
+#pragma unroll
+      for (int j = 0; j < TM; ++j) sx[j] = *(const uint32_t*)(ss + xsc + j * 32 * SRowB);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) sv[i] = *(const uint32_t*)(ss + wsc + i * 32 * SRowB);
+      if (it * 8 + 8 > kb) {   // the padding of a scale row is not a scale
+#pragma unroll
+        for (int j = 0; j < TM; ++j) sx[j] = keep_blocks(sx[j], it * 8 + 4 * h, kb);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) sv[i] = keep_blocks(sv[i], it * 8 + 4 * h, kb);
+      }
+      u32x4 xo[2][TM], wo[2][TN];
+      auto read = [&](int buf, int j) {
+        const uint32_t c = sw ^ (uint32_t)(j << 4);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) wo[buf][i] = *(const u32x4*)(sb + wrow + c + i * 32 * kRowB);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) xo[buf][i] = *(const u32x4*)(sb + xrow + c + i * 32 * kRowB);
+      };
+      auto step = [&](auto jc) {
+        constexpr int J = decltype(jc)::value;
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+            acc[i][j] = mfma_mx32<J>(wo[J & 1][i], xo[J & 1][j], acc[i][j], sv[i], sx[j]);
+      };
+      read(0, 0);
+      read(1, 1);
+      step(std::integral_constant<int, 0>());
+      read(0, 2);
+      step(std::integral_constant<int, 1>());
+      read(1, 3);
+      step(std::integral_constant<int, 2>());
+      step(std::integral_constant<int, 3>());
+      // a step's operand reads go before the products of the step before it
+      __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, TN * TM, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, TN * TM, 0);
+      if (it + 1 < kt) slot = slot + 1 == NST ? 0 : slot + 1;
+    }
+
+    // wait states between the last MFMA and the first vector read of its result
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    // The tile goes to memory through the LDS stage just read, so that a
+    // store takes whole lines of y: 16 bytes a lane, a row's lanes side by
+    // side. 16-byte chunks of a row are held at chunk ^ (row & 31), so that
+    // neither the 32 rows a wave writes at a time nor the row it reads meets
+    // a bank twice.
+    constexpr int kElem = D::kBytes;
+    constexpr int NEED = (BM * BN * kElem + kStageB - 1) / kStageB;
+    constexpr int PJ = NEED < TM ? NEED : TM, PI = (NEED + PJ - 1) / PJ;   // passes
+    constexpr int TPJ = TM / PJ, TPI = TN / PI;             // of a wave and pass
+    constexpr int CW = TPI * 32 * kElem / 16;               // chunks of a wave's columns
+    constexpr int CH = WN * CW;                             // chunks of a row
+    constexpr int MASK = CH < 32 ? CH - 1 : 31;
+    static_assert(WM * TPJ * 32 * CH * 16 <= kStageB && TM % PJ == 0 && TN % PI == 0 &&
+                      (CH & (CH - 1)) == 0 && 64 * NW % CH == 0, "a pass fits a stage");
+    char* eb = lds + slot * kStageB;
+    slot = slot + 1 == NST ? 0 : slot + 1;
+    const bool whole = cur.mrows == BM && cur.ncols == BN;
+    char* yb = (char*)a.y + ((int64_t)cur.row * a.N + cur.n0) * kElem;
+    // addresses of this part are formed here, not kept over the main loop
+    int te = tid;
+    asm volatile("" : "+v"(te));
+    const int me = te & 31, he = te >> 5 & 1;
+#pragma unroll
+    for (int p = 0; p < PJ * PI; ++p) {
+      const int pj = p % PJ, pi = p / PJ;
+      lds_barrier();
+#pragma unroll
+      for (int j = 0; j < TPJ; ++j) {
+        const int lr = (wm * TPJ + j) * 32 + me;
+#pragma unroll
+        for (int i = 0; i < TPI; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& z = acc[pi * TPI + i][pj * TPJ + j];
+            const int byte = (wn * TPI * 32 + i * 32 + 8 * q + 4 * he) * kElem;
+            char* dst = eb + lr * (CH * 16) + (((byte >> 4) ^ (lr & MASK)) << 4) + (byte & 15);
+            if constexpr (kElem == 2)
+              *(u32x2*)dst = u32x2{pack_bf16x2(z[4 * q], z[4 * q + 1]),
+                                   pack_bf16x2(z[4 * q + 2], z[4 * q + 3])};
+            else
+              *(f32x4*)dst = f32x4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+          }
+      }
+      lds_barrier();
+#pragma unroll
+      for (int k = 0; k < WM * TPJ * 32 * CH / (64 * NW); ++k) {
+        const int lr = te / CH + k * (64 * NW / CH), ch = te % CH;
+        const int r = (lr / (TPJ * 32) * TM + pj * TPJ) * 32 + lr % (TPJ * 32);
+        const int c = ((ch / CW * TN + pi * TPI) * 32 * kElem / 16 + ch % CW) * (16 / kElem);
+        const char* src = eb + lr * (CH * 16) + ((ch ^ (lr & MASK)) << 4);
+        char* dst = yb + (uint32_t)(r * a.N + c) * (uint32_t)kElem;   // below 2^30
+        // y's rows start on any element: 16 bytes go to any element's address
+        if (whole || (r < cur.mrows && c + 16 / kElem <= cur.ncols)) {
+          __builtin_nontemporal_store(*(const u32x4*)src, (u32x4_any*)dst);
+        } else if (r < cur.mrows) {
+          for (int u = 0; u < cur.ncols - c; ++u) {
+            if constexpr (kElem == 2)
+              ((uint16_t*)dst)[u] = ((const uint16_t*)src)[u];
+            else
+              ((uint32_t*)dst)[u] = ((const uint32_t*)src)[u];
+          }
+        }
+      }
+    }
+    if (!has_ld) break;   // no tile was fetched after this one
+    cur = ld;
+  }
+}
+
+template <typename D, int BM, int BN, int WM, int WN, int NST, bool SCREG>
+hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int cus) {
+  constexpr int NW = WM * WN;
+  constexpr int lds = lds_bytes<BM, BN, NW, NST, SCREG>();
+  const int64_t mt = (a.rows + BM - 1) / BM + (a.offsets ? a.E : 0);
+  const int64_t nt = (a.N + BN - 1) / BN;
+  if (mt * nt > 0x7fffffff) return hipErrorInvalidValue;
+  constexpr int occ = occupancy<BM, BN, NW, NST, SCREG>();
+  const int64_t grid = std::min<int64_t>(8 * ((mt * nt + 7) / 8), (int64_t)cus * occ / 8 * 8);
+  const void* f = (const void*)k_mx_tile<D, BM, BN, WM, WN, NST, SCREG>;
+  const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_mx_tile<D, BM, BN, WM, WN, NST, SCREG>), dim3((unsigned)grid),
+                     dim3(64 * NW), lds, stream, a, mx_scale_row(a.K), (int)nt);
+  return hipGetLastError();
+}
+
+// Tiles and depths by the sizes, mt x nt tiles of y for the compute units to
+// share. Every choice gives the same y. Measured (us, us of the others):
+//   256 x 256, where they fill the chip: 2048 x 6144 x 4096 38 (128^2: 45)
+//   128 x 128, two workgroups a unit: 512 rows of 8 experts x 28672 x 4096
+//     124 (128 x 256: 134, 64 x 128: 142, 256^2: 154)
+//   64 x 64, four stages, where every tile has a unit to itself: 1 x 6144 x
+//     4096 8.8 (64 x 128, three stages: 13, 128^2: 20)
+//   64 x 128, three stages, where those have: 30 x 19878 x 9088 36 (64^2: 44)
+//   64 x 64, scales by way of registers, for more tiles than units: 91 rows
+//     of 14 experts x 7390 x 8576 108 (64 x 128: 113, 128^2: 118); 64 x 128
+//     where the rows fill it: 1024 x 4096 x 4096 17 (64^2: 21, 128^2: 20)
+template <typename D>
+hipError_t launch_by_size(const MxArgs& a, hipStream_t stream) {
+  int cus = 0;
+  const hipError_t ec = compute_units(&cus);
+  if (ec != hipSuccess) return ec;
+  const int used = std::min(a.E, a.rows);   // experts with rows, at most
+  const int avg = a.rows / used;
+  auto tiles = [&](int bm, int bn) {
+    const int64_t mt = (a.rows + bm - 1) / bm + (a.offsets ? used / 2 : 0);
+    return std::max<int64_t>(mt, used) * ((a.N + bn - 1) / bn);
+  };
+  // a group of scale registers is 16 bytes of a row at the least, and a walk
+  // through NST stages needs tiles of NST - 1
+  if (a.K < 512) {
+    if (avg > 32 && tiles(128, 128) >= cus) return launch_tile<D, 128, 128, 2, 2, 2, false>(a, stream, cus);
+    return launch_tile<D, 64, 128, 2, 2, 2, false>(a, stream, cus);
+  }
+  if (avg >= 192 && tiles(256, 256) * 4 >= cus * 3)
+    return launch_tile<D, 256, 256, 4, 2, 2, true>(a, stream, cus);
+  if (avg >= 48 && tiles(128, 128) * 4 >= cus * 5)
+    return launch_tile<D, 128, 128, 2, 2, 2, true>(a, stream, cus);
+  if (a.K > 512 && tiles(64, 64) * 8 <= cus * 9)
+    return launch_tile<D, 64, 64, 2, 2, 4, false>(a, stream, cus);
+  if (tiles(64, 128) <= cus) return launch_tile<D, 64, 128, 2, 2, 3, false>(a, stream, cus);
+  if (avg > 64) return launch_tile<D, 64, 128, 2, 2, 2, true>(a, stream, cus);
+  return launch_tile<D, 64, 64, 2, 2, 2, true>(a, stream, cus);
 }
 
 hipError_t launch_mxfp4_linear(int dtype, const MxArgs& a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  const int sld = mx_scale_row(a.K);
-  // tiles of a segmented batch: one more per segment for its ragged end
-  const int64_t mt = (a.rows + 63) / 64 + (a.offsets ? a.E + 2 : 0);
-  const int64_t nt = (a.N + 63) / 64;
-  if (mt > 65535 * 4 || nt > 0x7fffffff) return hipErrorInvalidValue;
-#define GO(D)                                                                                \
-  hipLaunchKernelGGL(k_mx_simple<D>, dim3((unsigned)nt, (unsigned)mt), dim3(256), 0, stream, a, sld)
-  if (dtype == 1) GO(BF16); else GO(F32);
-#undef GO
-  return hipGetLastError();
+  return dtype == 1 ? launch_by_size<BF16>(a, stream) : launch_by_size<F32>(a, stream);
 }
 
 }  // namespace lora
