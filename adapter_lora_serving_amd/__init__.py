@@ -157,7 +157,8 @@ def _dev(*tensors):
 
 def _stream(dev) -> int:
     import torch
-    return torch.cuda.current_stream(dev).cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # 0.1 us in place of 2
+    return raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _ptr(t) -> int:

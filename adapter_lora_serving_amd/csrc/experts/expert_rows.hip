@@ -13,6 +13,138 @@
 
 namespace lora {
 
+// Where the sort by expert puts choice i: its row, or none for a dead one.
+__device__ __forceinline__ void put_row(int i, int k, int row, bool live,
+                                        const int32_t* __restrict__ token_slot,
+                                        int32_t* __restrict__ row_token,
+                                        int32_t* __restrict__ positions,
+                                        int32_t* __restrict__ row_slot) {
+  const int t = i / k;
+  row_token[row] = t;
+  positions[i] = live ? row : -1;
+  if (row_slot) row_slot[row] = live ? token_slot[t] : -1;
+}
+
+// A decode step's few choices over few experts: one wave, no barrier (the
+// one-wave sort of the slot addressing, with the rows written in its place).
+// 512 choices of 8 experts: one launch in place of two.
+template <int G>
+__global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ ids, int n, int k,
+                                                  int E, const int32_t* __restrict__ token_slot,
+                                                  int32_t* __restrict__ row_token,
+                                                  int32_t* __restrict__ positions,
+                                                  int32_t* __restrict__ offsets,
+                                                  int32_t* __restrict__ row_slot) {
+  __shared__ int hist[kWave];
+  const int lane = lane_id();
+  const int nbits = 32 - __clz(E);
+  int raw[G], key[G], off[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int i = g * kWave + lane;
+    raw[g] = i < n ? ids[i] : -1;
+  }
+  hist[lane] = 0;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const GroupMatch m = match_raw(raw[g], g * kWave + lane < n, E, nbits);
+    key[g] = m.key < 0 ? 0 : m.key;   // lanes past n: any valid index, never used
+    off[g] = hist[key[g]] + m.rank;
+    __builtin_amdgcn_wave_barrier();
+    if (m.leader) hist[m.key] += m.count;   // distinct keys: no two leaders collide
+    __builtin_amdgcn_wave_barrier();
+  }
+  const int c = lane <= E ? hist[lane] : 0;
+  const int start = wave_inclusive_scan(c) - c;
+  if (lane <= E) offsets[lane] = start;
+  __builtin_amdgcn_wave_barrier();
+  hist[lane] = start;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int i = g * kWave + lane;
+    if (i < n)
+      put_row(i, k, hist[key[g]] + off[g], key[g] < E, token_slot, row_token, positions, row_slot);
+  }
+}
+
+// Larger batches in one launch: a workgroup places 1024 choices and counts
+// all n of them for itself, those before its own apart from the rest, so no
+// workgroup waits for another. The counting reads n ids from L2 a workgroup:
+// 65536 choices are 64 workgroups of 256 KB each; past that the two passes
+// of the addressing count once.
+constexpr int kRowsBlock = 1024;
+constexpr int kRowsOneLaunch = 1 << 16;
+
+__global__ __launch_bounds__(kRowsBlock) void k_rows_block(
+    const int32_t* __restrict__ ids, int n, int k, int E, const int32_t* __restrict__ token_slot,
+    int32_t* __restrict__ row_token, int32_t* __restrict__ positions,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ row_slot) {
+  extern __shared__ int smem[];
+  const int S1 = E + 1;
+  int* cnt = smem;               // [16][S1] per-wave counts, then offsets in the workgroup
+  int* before = cnt + 16 * S1;   // [S1] choices before this workgroup's
+  int* rest = before + S1;       // [S1] the others
+  int* scratch = rest + S1;      // [20]
+  const int tid = threadIdx.x;
+  const int w = tid / kWave;
+  const int nbits = 32 - __clz(E);
+  const int own0 = blockIdx.x * kRowsBlock;
+  for (int i = tid; i < 18 * S1; i += kRowsBlock) smem[i] = 0;
+  const int i0 = own0 + tid;
+  const GroupMatch g = match_raw(i0 < n ? ids[i0] : -1, i0 < n, E, nbits);
+  __syncthreads();
+  if (g.leader) cnt[w * S1 + g.key] += g.count;   // distinct keys: no collision
+  auto count = [&](int i, int id) {
+    const int key = id >= 0 && id < E ? id : E;
+    atomicAdd(i < own0 ? before + key : rest + key, 1);
+  };
+  // whole vectors from the first 16-byte boundary on, single ids around them
+  const int head = min(n, (int)(-(reinterpret_cast<intptr_t>(ids) >> 2) & 3));
+  const int tail = head + ((n - head) & ~3);
+#pragma unroll 4
+  for (int i = head + tid * 4; i < tail; i += kRowsBlock * 4) {
+    const u32x4 v = *(const u32x4*)(ids + i);
+    count(i, (int)v.x);
+    count(i + 1, (int)v.y);
+    count(i + 2, (int)v.z);
+    count(i + 3, (int)v.w);
+  }
+  if (tid < head) count(tid, ids[tid]);
+  if (tail + tid < n) count(tail + tid, ids[tail + tid]);
+  __syncthreads();
+  int tot = 0;   // key tid (S1 <= 1025: the last key by thread 0 below)
+  auto offsets_of = [&](int key) {
+    int run = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int c = cnt[q * S1 + key];
+      cnt[q * S1 + key] = run;
+      run += c;
+    }
+  };
+  if (tid < E) {
+    tot = before[tid] + rest[tid];
+    offsets_of(tid);
+  }
+  if (tid == 0) offsets_of(E);
+  int live = 0;
+  const int start = block_exclusive_scan(tid < E ? tot : 0, scratch, &live);
+  if (tid < E) {
+    before[tid] += start;
+    if (blockIdx.x == 0) offsets[tid] = start;
+  }
+  if (tid == 0) {
+    before[E] += live;
+    if (blockIdx.x == 0) offsets[E] = live;
+  }
+  __syncthreads();
+  if (i0 < n)
+    put_row(i0, k, before[g.key] + cnt[w * S1 + g.key] + g.rank, g.key < E, token_slot, row_token,
+            positions, row_slot);
+}
+
 // row_token holds the sorted choices (token * k + j) on entry and the tokens
 // on return; every thread turns its own.
 __global__ __launch_bounds__(256) void k_rows_finish(int n, int k, int E,
@@ -23,25 +155,45 @@ __global__ __launch_bounds__(256) void k_rows_finish(int n, int k, int E,
                                                      int32_t* __restrict__ row_slot) {
   const int r = blockIdx.x * 256 + threadIdx.x;
   if (r >= n) return;
-  const int choice = row_token[r];
-  const int t = choice / k;
-  const bool live = r < offsets[E];
-  row_token[r] = t;
-  positions[choice] = live ? r : -1;
-  if (row_slot) row_slot[r] = live ? token_slot[t] : -1;
+  put_row(row_token[r], k, r, r < offsets[E], token_slot, row_token, positions, row_slot);
 }
 
 size_t expert_rows_workspace_bytes(int64_t T, int k, int E) {
-  return addressing_workspace_bytes(T * k, E);
+  return T * k <= kRowsOneLaunch ? 0 : addressing_workspace_bytes(T * k, E);
 }
 
 hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int32_t* token_slot,
                               int32_t* row_token, int32_t* positions, int32_t* offsets,
                               int32_t* row_slot, void* ws, hipStream_t stream) {
   const int n = T * k;
+  if (n <= 16 * kWave && E < kWave) {
+#define W(GV)                                                                              \
+  hipLaunchKernelGGL(k_rows_wave<GV>, dim3(1), dim3(kWave), 0, stream, ids, n, k, E, token_slot, \
+                     row_token, positions, offsets, row_slot)
+    const int groups = (n + kWave - 1) / kWave;
+    if (groups <= 1) W(1);
+    else if (groups <= 2) W(2);
+    else if (groups <= 4) W(4);
+    else if (groups <= 8) W(8);
+    else W(16);
+#undef W
+    return hipGetLastError();
+  }
+  if (n <= kRowsOneLaunch) {
+    const int nb = n == 0 ? 1 : (n + kRowsBlock - 1) / kRowsBlock;
+    const size_t lds = ((size_t)18 * (E + 1) + 20) * sizeof(int);
+    if (lds > 65536) {
+      const hipError_t e = hipFuncSetAttribute((const void*)k_rows_block,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(k_rows_block, dim3(nb), dim3(kRowsBlock), lds, stream, ids, n, k, E,
+                       token_slot, row_token, positions, offsets, row_slot);
+    return hipGetLastError();
+  }
   hipError_t e = launch_build_addressing(ids, n, E, row_token, offsets, ws,
                                          expert_rows_workspace_bytes(T, k, E), stream);
-  if (e != hipSuccess || n == 0) return e;
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_rows_finish, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, n, k,
                      E, offsets, token_slot, row_token, positions, row_slot);
   return hipGetLastError();

@@ -13,6 +13,7 @@
 // consecutive columns of one row of y. Products of two 4-bit values and the
 // powers of two are exact; the sums are fp32, y is rounded once.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 #include "lora_common.h"
 #include "experts.h"
@@ -62,13 +63,18 @@ __device__ __forceinline__ void lds_barrier() {
   barrier_no_fence();
 }
 
-// Compute units of the current device.
-hipError_t compute_units(int* n) {
-  int dev = 0;
-  const hipError_t e = hipGetDevice(&dev);
-  return e != hipSuccess
-             ? e
-             : hipDeviceGetAttribute(n, hipDeviceAttributeMultiprocessorCount, dev);
+// The current device and its compute units (asked for once per device).
+constexpr int kMaxDevices = 64;
+hipError_t compute_units(int* dev, int* n) {
+  static std::atomic<int> known[kMaxDevices];
+  const hipError_t e = hipGetDevice(dev);
+  if (e != hipSuccess) return e;
+  if (*dev < 0 || *dev >= kMaxDevices) return hipErrorInvalidDevice;
+  *n = known[*dev].load(std::memory_order_relaxed);
+  if (*n > 0) return hipSuccess;
+  const hipError_t a = hipDeviceGetAttribute(n, hipDeviceAttributeMultiprocessorCount, *dev);
+  if (a == hipSuccess) known[*dev].store(*n, std::memory_order_relaxed);
+  return a;
 }
 
 }  // namespace
@@ -472,7 +478,7 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
 }
 
 template <typename D, int BM, int BN, int WM, int WN, int NST, bool SCREG>
-hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int cus) {
+hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int dev, int cus) {
   constexpr int NW = WM * WN;
   constexpr int lds = lds_bytes<BM, BN, NW, NST, SCREG>();
   const int64_t mt = (a.rows + BM - 1) / BM + (a.offsets ? a.E : 0);
@@ -481,8 +487,14 @@ hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int cus) {
   constexpr int occ = occupancy<BM, BN, NW, NST, SCREG>();
   const int64_t grid = std::min<int64_t>(8 * ((mt * nt + 7) / 8), (int64_t)cus * occ / 8 * 8);
   const void* f = (const void*)k_mx_tile<D, BM, BN, WM, WN, NST, SCREG>;
-  const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (e != hipSuccess) return e;
+  if (lds > 65536) {   // said once per device
+    static std::atomic<uint64_t> said{0};
+    if (!(said.load(std::memory_order_relaxed) >> dev & 1)) {
+      const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return e;
+      said.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    }
+  }
   hipLaunchKernelGGL((k_mx_tile<D, BM, BN, WM, WN, NST, SCREG>), dim3((unsigned)grid),
                      dim3(64 * NW), lds, stream, a, mx_scale_row(a.K), (int)nt);
   return hipGetLastError();
@@ -501,8 +513,8 @@ hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int cus) {
 //     where the rows fill it: 1024 x 4096 x 4096 17 (64^2: 21, 128^2: 20)
 template <typename D>
 hipError_t launch_by_size(const MxArgs& a, hipStream_t stream) {
-  int cus = 0;
-  const hipError_t ec = compute_units(&cus);
+  int dev = 0, cus = 0;
+  const hipError_t ec = compute_units(&dev, &cus);
   if (ec != hipSuccess) return ec;
   const int used = std::min(a.E, a.rows);   // experts with rows, at most
   const int avg = a.rows / used;
@@ -513,18 +525,19 @@ hipError_t launch_by_size(const MxArgs& a, hipStream_t stream) {
   // a group of scale registers is 16 bytes of a row at the least, and a walk
   // through NST stages needs tiles of NST - 1
   if (a.K < 512) {
-    if (avg > 32 && tiles(128, 128) >= cus) return launch_tile<D, 128, 128, 2, 2, 2, false>(a, stream, cus);
-    return launch_tile<D, 64, 128, 2, 2, 2, false>(a, stream, cus);
+    if (avg > 32 && tiles(128, 128) >= cus)
+      return launch_tile<D, 128, 128, 2, 2, 2, false>(a, stream, dev, cus);
+    return launch_tile<D, 64, 128, 2, 2, 2, false>(a, stream, dev, cus);
   }
   if (avg >= 192 && tiles(256, 256) * 4 >= cus * 3)
-    return launch_tile<D, 256, 256, 4, 2, 2, true>(a, stream, cus);
+    return launch_tile<D, 256, 256, 4, 2, 2, true>(a, stream, dev, cus);
   if (avg >= 48 && tiles(128, 128) * 4 >= cus * 5)
-    return launch_tile<D, 128, 128, 2, 2, 2, true>(a, stream, cus);
+    return launch_tile<D, 128, 128, 2, 2, 2, true>(a, stream, dev, cus);
   if (a.K > 512 && tiles(64, 64) * 8 <= cus * 9)
-    return launch_tile<D, 64, 64, 2, 2, 4, false>(a, stream, cus);
-  if (tiles(64, 128) <= cus) return launch_tile<D, 64, 128, 2, 2, 3, false>(a, stream, cus);
-  if (avg > 64) return launch_tile<D, 64, 128, 2, 2, 2, true>(a, stream, cus);
-  return launch_tile<D, 64, 64, 2, 2, 2, true>(a, stream, cus);
+    return launch_tile<D, 64, 64, 2, 2, 4, false>(a, stream, dev, cus);
+  if (tiles(64, 128) <= cus) return launch_tile<D, 64, 128, 2, 2, 3, false>(a, stream, dev, cus);
+  if (avg > 64) return launch_tile<D, 64, 128, 2, 2, 2, true>(a, stream, dev, cus);
+  return launch_tile<D, 64, 64, 2, 2, 2, true>(a, stream, dev, cus);
 }
 
 hipError_t launch_mxfp4_linear(int dtype, const MxArgs& a, hipStream_t stream) {

@@ -30,45 +30,92 @@ __device__ __forceinline__ uint32_t order_key(float c) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <int W>
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < W; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+// v of the lane N places on in its row of 16 lanes (a rotation).
+template <int N>
+__device__ __forceinline__ uint32_t ror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 | N, 0xf, 0xf, false);
+}
+template <int N>
+__device__ __forceinline__ float ror(float v) {
+  return __uint_as_float(ror<N>(__float_as_uint(v)));
+}
+template <int N>
+__device__ __forceinline__ double ror(double v) {
+  const u32x2 u = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{ror<N>(u.x), ror<N>(u.y)});
+}
+
+// op over the L lanes (16 or 64) of a token, the result in all of them.
+template <int L, typename T, typename Op>
+__device__ __forceinline__ T over_lanes(T v, Op op) {
+  v = op(v, ror<8>(v));
+  v = op(v, ror<4>(v));
+  v = op(v, ror<2>(v));
+  v = op(v, ror<1>(v));
+  if constexpr (L == 64) {
+    v = op(v, __shfl_xor(v, 16));
+    v = op(v, __shfl_xor(v, 32));
+  }
   return v;
 }
-template <int W>
-__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+
+// The choice score that an order key stands for.
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// One of a lane's V consecutive values of a row of E, -inf past its end.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int e0, int E, float* x) {
+  if (E % V == 0) {   // a row starts on V values: whole vectors
+    if (e0 >= E) {
 #pragma unroll
-  for (int d = 1; d < W; d <<= 1) v = min(v, (uint32_t)__shfl_xor((int)v, d));
-  return v;
+      for (int i = 0; i < V; ++i) x[i] = -kInf;
+      return;
+    }
+    struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack { T v[V]; };
+    const Pack p = *(const Pack*)(row + e0);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (sizeof(T) == 2) x[i] = __uint_as_float((uint32_t)p.v[i] << 16);
+      else x[i] = p.v[i];
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    x[i] = -kInf;
+    if (e0 + i < E) {
+      if constexpr (sizeof(T) == 2) x[i] = __uint_as_float((uint32_t)row[e0 + i] << 16);
+      else x[i] = row[e0 + i];
+    }
+  }
 }
 
 }  // namespace
 
-// L lanes per token (16 or 64), V consecutive experts per lane (E <= L * V).
+// L lanes per token (16 or 64: reductions stay in the lanes' rows), V
+// consecutive experts per lane (E <= L * V). The scores also go to LDS, where
+// a choice's weight is looked up by its expert.
 template <typename T, int L, int V>
-__global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits_,
+__global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
                                                const float* __restrict__ bias, RouteArgs a,
                                                uint32_t gmagic, int32_t* __restrict__ ids,
                                                float* __restrict__ weights) {
+  __shared__ __attribute__((aligned(16))) float score[256 * V];
+  __shared__ int chosen[256 / L][kMaxTopK];
   const int l = threadIdx.x % L;
-  const int t = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int tok = threadIdx.x / L;
+  const int t = blockIdx.x * (256 / L) + tok;
   const bool live = t < a.T;
-  const int64_t base = (int64_t)(live ? t : a.T - 1) * a.E;
   const int e0 = l * V;
+  auto fmax2 = [](float p, float q) { return fmaxf(p, q); };
+  auto umax2 = [](uint32_t p, uint32_t q) { return max(p, q); };
 
   float x[V];
+  load_row<T, V>(logits + (int64_t)(live ? t : a.T - 1) * a.E, e0, a.E, x);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    x[i] = -kInf;
-    if (e0 + i < a.E) {
-      if constexpr (sizeof(T) == 2)
-        x[i] = __uint_as_float((uint32_t)((const uint16_t*)logits_)[base + e0 + i] << 16);
-      else
-        x[i] = ((const float*)logits_)[base + e0 + i];
-      x[i] = x[i] != x[i] ? -kInf : fminf(x[i], __FLT_MAX__);
-    }
-  }
+  for (int i = 0; i < V; ++i) x[i] = x[i] != x[i] ? -kInf : fminf(x[i], __FLT_MAX__);
 
   // scores (0 where not available) and the order keys of the choice scores
   float s[V];
@@ -79,56 +126,81 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits_,
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    m = over_lanes<L>(m, fmax2);
     double z = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       s[i] = x[i] == -kInf ? 0.0f : expf(x[i] - m);
       z += (double)s[i];
     }
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) z += __shfl_xor(z, d);
-    const float zf = (float)z;
+    const float zf = (float)over_lanes<L>(z, [](double p, double q) { return p + q; });
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = zf > 0.0f ? s[i] / zf : 0.0f;
   }
   uint32_t key[V];
+  float b[V];
+  if (bias) {
+    load_row<float, V>(bias, e0, a.E, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] += s[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = s[i];
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    float c = s[i];
-    if (bias && e0 + i < a.E) c += bias[e0 + i];
-    key[i] = (x[i] == -kInf || c != c || c == -kInf) ? 0u : order_key(c);
+    score[threadIdx.x * V + i] = s[i];
+    key[i] = (x[i] == -kInf || b[i] != b[i] || b[i] == -kInf) ? 0u : order_key(b[i]);
   }
 
   if (a.top_groups < a.groups) {
     // lane g of the token's lanes keeps the worth of group g, then its rank
     // among the groups says whether it stays
     float worth = -kInf;
-    int grp[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) grp[i] = (int)(((uint64_t)(uint32_t)(e0 + i) * gmagic) >> 21);
-    for (int g = 0; g < a.groups; ++g) {
-      uint32_t b0 = 0, b1 = 0;   // two best keys of the group
+    const int gs = a.E / a.groups;
+    auto worth_of = [&](uint32_t b0, uint32_t b1) {
+      const float v = b0 ? key_value(b0) : -kInf;
+      return a.sum2 && b1 ? v + key_value(b1) : v;
+    };
+    if (gs % V == 0) {
+      // every lane's experts are of one group, gs / V lanes side by side hold
+      // it: two best of the lane, then of the group's lanes
+      uint32_t b0 = 0, b1 = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const uint32_t q = grp[i] == g ? key[i] : 0u;
-        b1 = max(b1, min(b0, q));
-        b0 = max(b0, q);
+        b1 = max(b1, min(b0, key[i]));
+        b0 = max(b0, key[i]);
       }
+      const int per = gs / V;
+      const int first = l / per * per;
+      uint32_t g0 = 0, g1 = 0;
+      for (int q = 0; q < per; ++q) {
+        const int src = min(first + q, L - 1);
+        const uint32_t o0 = (uint32_t)__shfl((int)b0, src, L);
+        const uint32_t o1 = (uint32_t)__shfl((int)b1, src, L);
+        g1 = max(max(g1, o1), min(g0, o0));
+        g0 = max(g0, o0);
+      }
+      worth = __shfl(worth_of(g0, g1), min(l * per, L - 1), L);
+      if (l >= a.groups) worth = -kInf;
+    } else {
+      for (int g = 0; g < a.groups; ++g) {
+        uint32_t b0 = 0, b1 = 0;   // two best keys of the group
 #pragma unroll
-      for (int d = 1; d < L; d <<= 1) {
-        const uint32_t o0 = (uint32_t)__shfl_xor((int)b0, d);
-        const uint32_t o1 = (uint32_t)__shfl_xor((int)b1, d);
-        b1 = max(max(b1, o1), min(b0, o0));
-        b0 = max(b0, o0);
+        for (int i = 0; i < V; ++i) {
+          const int grp = (int)(((uint64_t)(uint32_t)(e0 + i) * gmagic) >> 21);
+          const uint32_t q = grp == g ? key[i] : 0u;
+          b1 = max(b1, min(b0, q));
+          b0 = max(b0, q);
+        }
+        // the second best is the best but one lane's best, or that lane's second
+        const uint32_t top = over_lanes<L>(b0, umax2);
+        const uint64_t eq = __ballot(b0 == top) >> (lane_id() & ~(L - 1));
+        const bool mine = l == __ffsll((unsigned long long)eq) - 1;
+        const uint32_t sec = over_lanes<L>(mine ? b1 : b0, umax2);
+        const float wv = worth_of(top, sec);
+        if (l == g) worth = wv;
       }
-      auto val = [](uint32_t k) {
-        return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-      };
-      float wv = b0 ? val(b0) : -kInf;
-      if (a.sum2 && b0 && b1) wv += val(b1);
-      if (l == g) worth = wv;
     }
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
@@ -138,48 +210,48 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits_,
     const uint64_t all = __ballot(l < a.groups && rank < a.top_groups);
     const uint32_t keep = (uint32_t)(all >> (lane_id() & ~(L - 1)));
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!((keep >> (grp[i] & 31)) & 1u)) key[i] = 0u;
+    for (int i = 0; i < V; ++i) {
+      const int grp = (int)(((uint64_t)(uint32_t)(e0 + i) * gmagic) >> 21);
+      if (!((keep >> (grp & 31)) & 1u)) key[i] = 0u;
+    }
   }
 
-  // top_k rounds: the largest key, its lowest expert, out with it
-  int my_id = -1;        // lane r keeps the r-th choice (r and r + L where top_k > L)
-  float my_w = 0.0f;
-  int my_id2 = -1;
-  float my_w2 = 0.0f;
-  float total = 0.0f;
+  // top_k rounds: the largest key, its lowest expert, out with it. A lane
+  // holds consecutive experts, so the lowest lane that holds the largest key
+  // holds the lowest expert of that key.
   for (int r = 0; r < a.k; ++r) {
     uint32_t best = 0;
     int bi = 0;
-    float bs = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i] > best) { best = key[i]; bi = i; bs = s[i]; }
-    const uint32_t top = row_max<L>(best);
-    // consecutive experts per lane: the lowest lane that holds the largest
-    // key holds the lowest expert of that key
-    const uint32_t lane = row_min<L>(top != 0u && best == top ? (uint32_t)l : 0xffffu);
-    const int src = lane == 0xffffu ? 0 : (int)lane;
-    const int id = lane == 0xffffu ? -1 : __shfl(e0 + bi, src, L);
-    const float w = lane == 0xffffu ? 0.0f : __shfl(bs, src, L);
-    if ((uint32_t)l == lane) {
+      if (key[i] > best) { best = key[i]; bi = i; }
+    const uint32_t top = over_lanes<L>(best, umax2);
+    const uint64_t eq = __ballot(best == top) >> (lane_id() & ~(L - 1));
+    if (l == __ffsll((unsigned long long)eq) - 1) {
+      chosen[tok][r] = top ? e0 + bi : -1;
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (i == bi) key[i] = 0u;
     }
-    if (l == r) { my_id = id; my_w = w; }
-    if (l + L == r) { my_id2 = id; my_w2 = w; }
-    total += w;
   }
+  // the token's lanes are lanes of one wave, whose LDS operations are in order
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  float total = 0.0f;
+  if (a.renorm)
+    for (int r = 0; r < a.k; ++r) {
+      const int id = chosen[tok][r];
+      total += id < 0 ? 0.0f : score[tok * L * V + id];
+    }
   const float div = a.renorm ? total : 1.0f;
-  auto put = [&](int r, int id, float w) {
-    if (live && r < a.k) {
+  for (int r = l; r < a.k; r += L) {
+    const int id = chosen[tok][r];
+    const float w = id < 0 ? 0.0f : score[tok * L * V + id];
+    if (live) {
       ids[(int64_t)t * a.k + r] = id;
       weights[(int64_t)t * a.k + r] = div > 0.0f ? w / div * a.scaling : 0.0f;
     }
-  };
-  put(l, my_id, my_w);
-  if (L < kMaxTopK) put(l + L, my_id2, my_w2);
+  }
 }
 
 hipError_t launch_route_experts(int dtype, const void* logits, const float* bias,
@@ -191,7 +263,7 @@ hipError_t launch_route_experts(int dtype, const void* logits, const float* bias
   const uint32_t gmagic = (1u << 21) / gs + 1u;
 #define LAUNCH(TT, LV, VV)                                                                     \
   hipLaunchKernelGGL((k_route<TT, LV, VV>), dim3((unsigned)((a.T + 256 / LV - 1) / (256 / LV))), \
-                     dim3(256), 0, stream, logits, bias, a, gmagic, ids, weights)
+                     dim3(256), 0, stream, (const TT*)logits, bias, a, gmagic, ids, weights)
 #define BY_E(TT)                              \
   do {                                        \
     if (a.E <= 16) LAUNCH(TT, 16, 1);         \
