@@ -1,4 +1,5 @@
-"""Build the HIP library liblora_mi355x.so in-tree for gfx950.
+"""Build the HIP library liblora_mi355x.so in-tree for gfx950, and the
+compiled Python binding of the routed-expert operators, _experts.so.
 
     python -m adapter_lora_serving_amd.build
 
@@ -59,17 +60,51 @@ def _compile(src: str) -> str:
     return obj
 
 
+BINDING_PATH = os.path.join(PKG, "_experts.so")
+
+
+def _compile_binding() -> str:
+    """The host object of the compiled binding (torch's and Python's headers)."""
+    import sysconfig
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "experts_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"],
+           "-c", os.path.join(CSRC, "experts", "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on experts/binding.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN",
+           "-L", libs, "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(jobs: int = 8) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
-    with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(srcs)))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(srcs) + 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding = binding.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding)
     return LIB_PATH
 
 
