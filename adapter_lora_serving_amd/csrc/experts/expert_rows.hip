@@ -13,24 +13,29 @@
 
 namespace lora {
 
-// Where the sort by expert puts choice i: its row, or none for a dead one.
-__device__ __forceinline__ void put_row(int i, int k, int row, bool live,
-                                        const int32_t* __restrict__ token_slot,
+// Token of choice i: i / k as a product with kmul = ceil(2^32 / k) (0 for k =
+// 1), exact where i k^2 < 2^32: for the 2^16 choices of one launch at most.
+__device__ __forceinline__ int token_of(int i, uint32_t kmul) {
+  return kmul ? (int)__umulhi((uint32_t)i, kmul) : i;
+}
+
+// Where the sort by expert puts choice i of token t: its row, or none for a
+// dead one.
+__device__ __forceinline__ void put_row(int i, int t, int row, bool live, int slot,
                                         int32_t* __restrict__ row_token,
                                         int32_t* __restrict__ positions,
                                         int32_t* __restrict__ row_slot) {
-  const int t = i / k;
   row_token[row] = t;
   positions[i] = live ? row : -1;
-  if (row_slot) row_slot[row] = live ? token_slot[t] : -1;
+  if (row_slot) row_slot[row] = live ? slot : -1;
 }
 
 // A decode step's few choices over few experts: one wave, no barrier (the
 // one-wave sort of the slot addressing, with the rows written in its place).
 // 512 choices of 8 experts: one launch in place of two.
 template <int G>
-__global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ ids, int n, int k,
-                                                  int E, const int32_t* __restrict__ token_slot,
+__global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ ids, int n,
+                                                  uint32_t kmul, int E, const int32_t* __restrict__ token_slot,
                                                   int32_t* __restrict__ row_token,
                                                   int32_t* __restrict__ positions,
                                                   int32_t* __restrict__ offsets,
@@ -38,11 +43,12 @@ __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ id
   __shared__ int hist[kWave];
   const int lane = lane_id();
   const int nbits = 32 - __clz(E);
-  int raw[G], key[G], off[G];
+  int raw[G], slot[G], key[G], off[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int i = g * kWave + lane;
     raw[g] = i < n ? ids[i] : -1;
+    slot[g] = row_slot && i < n ? token_slot[token_of(i, kmul)] : -1;
   }
   hist[lane] = 0;
   __builtin_amdgcn_wave_barrier();
@@ -65,7 +71,8 @@ __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ id
   for (int g = 0; g < G; ++g) {
     const int i = g * kWave + lane;
     if (i < n)
-      put_row(i, k, hist[key[g]] + off[g], key[g] < E, token_slot, row_token, positions, row_slot);
+      put_row(i, token_of(i, kmul), hist[key[g]] + off[g], key[g] < E, slot[g], row_token,
+              positions, row_slot);
   }
 }
 
@@ -76,29 +83,32 @@ __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ id
 // of the addressing count once.
 constexpr int kRowsBlock = 1024;
 constexpr int kRowsOneLaunch = 1 << 16;
+constexpr int kCopies = 4;   // of the counters: neighbouring lanes add to others
 
 __global__ __launch_bounds__(kRowsBlock) void k_rows_block(
-    const int32_t* __restrict__ ids, int n, int k, int E, const int32_t* __restrict__ token_slot,
-    int32_t* __restrict__ row_token, int32_t* __restrict__ positions,
+    const int32_t* __restrict__ ids, int n, uint32_t kmul, int E,
+    const int32_t* __restrict__ token_slot, int32_t* __restrict__ row_token, int32_t* __restrict__ positions,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_slot) {
   extern __shared__ int smem[];
   const int S1 = E + 1;
   int* cnt = smem;               // [16][S1] per-wave counts, then offsets in the workgroup
-  int* before = cnt + 16 * S1;   // [S1] choices before this workgroup's
-  int* rest = before + S1;       // [S1] the others
-  int* scratch = rest + S1;      // [20]
+  int* before = cnt + 16 * S1;        // [kCopies][S1] choices before this workgroup's
+  int* rest = before + kCopies * S1;  // [kCopies][S1] the others
+  int* scratch = rest + kCopies * S1; // [20]
   const int tid = threadIdx.x;
   const int w = tid / kWave;
   const int nbits = 32 - __clz(E);
   const int own0 = blockIdx.x * kRowsBlock;
-  for (int i = tid; i < 18 * S1; i += kRowsBlock) smem[i] = 0;
+  for (int i = tid; i < (16 + 2 * kCopies) * S1; i += kRowsBlock) smem[i] = 0;
   const int i0 = own0 + tid;
   const GroupMatch g = match_raw(i0 < n ? ids[i0] : -1, i0 < n, E, nbits);
+  const int t0 = token_of(min(i0, n), kmul);
+  const int slot = row_slot && i0 < n ? token_slot[t0] : -1;
   __syncthreads();
   if (g.leader) cnt[w * S1 + g.key] += g.count;   // distinct keys: no collision
   auto count = [&](int i, int id) {
     const int key = id >= 0 && id < E ? id : E;
-    atomicAdd(i < own0 ? before + key : rest + key, 1);
+    atomicAdd((i < own0 ? before : rest) + tid % kCopies * S1 + key, 1);
   };
   // whole vectors from the first 16-byte boundary on, single ids around them
   const int head = min(n, (int)(-(reinterpret_cast<intptr_t>(ids) >> 2) & 3));
@@ -123,11 +133,16 @@ __global__ __launch_bounds__(kRowsBlock) void k_rows_block(
       cnt[q * S1 + key] = run;
       run += c;
     }
+    int b = 0, r = 0;
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      b += before[q * S1 + key];
+      r += rest[q * S1 + key];
+    }
+    before[key] = b;
+    return b + r;
   };
-  if (tid < E) {
-    tot = before[tid] + rest[tid];
-    offsets_of(tid);
-  }
+  if (tid < E) tot = offsets_of(tid);
   if (tid == 0) offsets_of(E);
   int live = 0;
   const int start = block_exclusive_scan(tid < E ? tot : 0, scratch, &live);
@@ -141,7 +156,7 @@ __global__ __launch_bounds__(kRowsBlock) void k_rows_block(
   }
   __syncthreads();
   if (i0 < n)
-    put_row(i0, k, before[g.key] + cnt[w * S1 + g.key] + g.rank, g.key < E, token_slot, row_token,
+    put_row(i0, t0, before[g.key] + cnt[w * S1 + g.key] + g.rank, g.key < E, slot, row_token,
             positions, row_slot);
 }
 
@@ -155,7 +170,9 @@ __global__ __launch_bounds__(256) void k_rows_finish(int n, int k, int E,
                                                      int32_t* __restrict__ row_slot) {
   const int r = blockIdx.x * 256 + threadIdx.x;
   if (r >= n) return;
-  put_row(row_token[r], k, r, r < offsets[E], token_slot, row_token, positions, row_slot);
+  const int i = row_token[r], t = i / k;
+  const bool live = r < offsets[E];
+  put_row(i, t, r, live, row_slot && live ? token_slot[t] : -1, row_token, positions, row_slot);
 }
 
 size_t expert_rows_workspace_bytes(int64_t T, int k, int E) {
@@ -166,9 +183,11 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
                               int32_t* row_token, int32_t* positions, int32_t* offsets,
                               int32_t* row_slot, void* ws, hipStream_t stream) {
   const int n = T * k;
+  const uint32_t kmul = k == 1 ? 0u : (uint32_t)(((1ull << 32) + k - 1) / k);
   if (n <= 16 * kWave && E < kWave) {
 #define W(GV)                                                                              \
-  hipLaunchKernelGGL(k_rows_wave<GV>, dim3(1), dim3(kWave), 0, stream, ids, n, k, E, token_slot, \
+  hipLaunchKernelGGL(k_rows_wave<GV>, dim3(1), dim3(kWave), 0, stream, ids, n, kmul, E,          \
+                     token_slot, \
                      row_token, positions, offsets, row_slot)
     const int groups = (n + kWave - 1) / kWave;
     if (groups <= 1) W(1);
@@ -181,13 +200,13 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
   }
   if (n <= kRowsOneLaunch) {
     const int nb = n == 0 ? 1 : (n + kRowsBlock - 1) / kRowsBlock;
-    const size_t lds = ((size_t)18 * (E + 1) + 20) * sizeof(int);
+    const size_t lds = ((size_t)(16 + 2 * kCopies) * (E + 1) + 20) * sizeof(int);
     if (lds > 65536) {
       const hipError_t e = hipFuncSetAttribute((const void*)k_rows_block,
                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k_rows_block, dim3(nb), dim3(kRowsBlock), lds, stream, ids, n, k, E,
+    hipLaunchKernelGGL(k_rows_block, dim3(nb), dim3(kRowsBlock), lds, stream, ids, n, kmul, E,
                        token_slot, row_token, positions, offsets, row_slot);
     return hipGetLastError();
   }

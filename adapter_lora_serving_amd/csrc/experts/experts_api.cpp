@@ -11,6 +11,9 @@ namespace {
 
 constexpr int64_t kMaxI32 = 0x7fffffff;
 constexpr int64_t kMaxWidth = 1 << 20;   // columns or K of an operand
+// values of one quantisation: 2^31 threads of 8, with the scale row's padding
+// (at most 3 blocks in 4)
+constexpr int64_t kMaxValues = (int64_t)1 << 32;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -147,6 +150,7 @@ lora_status lora_quantize_mxfp4(int dtype, int32_t form, const void* x, int64_t 
   const lora_status st = check_mx(rows, K);
   if (st != LORA_OK) return st;
   if (x_rows < 0 || x_rows > kMaxI32) return LORA_ERR_INVALID_ARG;
+  if (rows * K > kMaxValues) return LORA_ERR_UNSUPPORTED;
   if (rows == 0) return LORA_OK;
   if (!x || !codes || !scales) return LORA_ERR_INVALID_ARG;
   if (form == LORA_QUANTIZE_GATHER ? (!row_index || x_rows < 1) : x_rows < rows)
@@ -163,6 +167,7 @@ lora_status lora_dequantize_mxfp4(int dtype, const uint8_t* codes, const uint8_t
   if (!dtype_ok(dtype)) return LORA_ERR_UNSUPPORTED;
   const lora_status st = check_mx(rows, K);
   if (st != LORA_OK) return st;
+  if (rows * K > kMaxValues) return LORA_ERR_UNSUPPORTED;
   if (rows == 0) return LORA_OK;
   if (!codes || !scales || !out) return LORA_ERR_INVALID_ARG;
   if (!aligned16(codes) || !aligned4(scales) || !aligned16(out)) return LORA_ERR_ALIGNMENT;

@@ -92,13 +92,52 @@ __device__ __forceinline__ void zero_dead_rows(const MxArgs& a) {
   }
 }
 
-// LDS of a tile kernel (stages, scale slots, scratch), and the workgroups of
+// Row tiles of BM rows over all experts, counted by every wave for itself (no
+// barrier, so that waves may call it at different times).
+template <int BM>
+__device__ __forceinline__ int count_tiles(const MxArgs& a) {
+  int tiles = 0;
+  for (int s = lane_id(); s < a.E; s += kWave) {
+    int beg, len;
+    segment_of(a.offsets, s, a.rows, beg, len);
+    tiles += (len + BM - 1) / BM;
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) tiles += __shfl_xor(tiles, d);
+  return __builtin_amdgcn_readfirstlane(tiles);
+}
+
+// Row tile `item` of the experts: its first row, rows and expert.
+template <int BM>
+__device__ __forceinline__ void find_tile(const MxArgs& a, int item, int& row, int& rows, int& e) {
+  const int lane = lane_id();
+  int before = 0;
+  row = rows = e = 0;
+  for (int s0 = 0; s0 < a.E; s0 += kWave) {
+    int beg = 0, len = 0;
+    if (s0 + lane < a.E) segment_of(a.offsets, s0 + lane, a.rows, beg, len);
+    const int tiles = (len + BM - 1) / BM;
+    const int upto = before + wave_inclusive_scan(tiles);
+    const uint64_t past = __ballot(upto > item);
+    if (past != 0) {
+      const int src = __ffsll((unsigned long long)past) - 1;
+      const int local = item - (__shfl(upto, src) - __shfl(tiles, src));
+      row = __builtin_amdgcn_readfirstlane(__shfl(beg, src) + local * BM);
+      rows = __builtin_amdgcn_readfirstlane(min(BM, __shfl(len, src) - local * BM));
+      e = __builtin_amdgcn_readfirstlane(s0 + src);
+      return;
+    }
+    before = __builtin_amdgcn_readfirstlane(__shfl(upto, kWave - 1));
+  }
+}
+
+// LDS of a tile kernel (stages, scale slots), and the workgroups of
 // it that a compute unit's 160 KB hold (at most 16 waves of them: with more,
 // fewer registers a wave than its accumulators and operands need)
 template <int BM, int BN, int NW, int NST, bool SCREG>
 constexpr int lds_bytes() {
   constexpr int SRowB = SCREG ? 16 : 8;
-  return NST * ((BM + BN) * kRowB + ((BM + BN) * SRowB / 256 + NW - 1) / NW * NW * 256) + 128;
+  return NST * ((BM + BN) * kRowB + ((BM + BN) * SRowB / 256 + NW - 1) / NW * NW * 256);
 }
 template <int BM, int BN, int NW, int NST, bool SCREG>
 constexpr int occupancy() {
@@ -111,10 +150,9 @@ constexpr int occupancy() {
 // runs on from one tile into the next, so a tile's first stage is on its way
 // while the tile before it is finished and stored.
 template <typename D, int BM, int BN, int WM, int WN, int NST, bool SCREG>
-__global__ __launch_bounds__(64 * WM * WN, (occupancy<BM, BN, WM * WN, NST, SCREG>() * WM * WN / 4)) void
+__global__ __launch_bounds__(64 * WM * WN, ((occupancy<BM, BN, WM * WN, NST, SCREG>() * WM * WN + 3) / 4)) void
 k_mx_tile(MxArgs a, int sld, int ntiles) {
   static_assert(!SCREG || NST == 2, "scale registers look one stage ahead");
-  static_assert(WM * WN % 2 == 0, "the swizzle of a wave's transfers is the same for all of them");
   constexpr int NW = WM * WN;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   constexpr int RPI = 8;                                    // rows of a transfer
@@ -128,7 +166,6 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   constexpr int kScaleB = SI * NW * 256;                    // scale bytes of a slot
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* lsc = lds + NST * kStageB;
-  int* scratch = (int*)(lsc + NST * kScaleB);
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const int w = wave_id();
@@ -138,15 +175,8 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
 
   // the experts' row tiles; rows of no expert become zero
   int mtiles = (a.rows + BM - 1) / BM;
-  SlotScan sc;
-  auto info = [&](int s, int* v) {
-    segment_of(a.offsets, s, a.rows, v[0], v[1]);
-    v[2] = 0;
-  };
-  auto count = [&](const int* v) { return (v[1] + BM - 1) / BM; };
   if (a.offsets) {
-    sc = scan_slots(a.E, info, count, scratch);
-    mtiles = sc.total;
+    mtiles = count_tiles<BM>(a);
     zero_dead_rows<D>(a);
   }
 
@@ -176,13 +206,7 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
     t.row = tm * BM;
     t.mrows = min(BM, a.rows - t.row);
     if (a.offsets) {
-      SlotItem it;
-      int v[3];
-      __syncthreads();   // scratch is free again
-      pick_item(sc, tm, info, count, scratch, it, v);
-      t.e = it.slot;
-      t.row = v[0] + it.local * BM;
-      t.mrows = min(BM, v[1] - it.local * BM);
+      find_tile<BM>(a, tm, t.row, t.mrows, t.e);
     }
     return t;
   };
@@ -203,7 +227,8 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   // for the products and reads of a 8192 x 28672 x 4096 product)
   const int pr = lane >> 3;
   auto swz = [](int row) { return row >> 1 & 7; };
-  const uint32_t pc = (uint32_t)((lane & 7) ^ swz(w * RPI + pr)) * 16u;
+  // of a wave's transfer i; the same for all of them but for a lone wave
+  auto pc = [&](int i) { return (uint32_t)((lane & 7) ^ swz((w + NW * i) * RPI + pr)) * 16u; };
   uint32_t xoff[XI], woff[WI], soff[SCREG ? 1 : SI];
   rsrc_t xs_r, ws_r;
   auto point_at = [&](const Tile& t) {
@@ -212,12 +237,12 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
       const int row = (w + NW * i) * RPI + pr;
-      xoff[i] = row < t.mrows ? (uint32_t)row * rowb + pc : kOOB;
+      xoff[i] = row < t.mrows ? (uint32_t)row * rowb + pc(i) : kOOB;
     }
 #pragma unroll
     for (int i = 0; i < WI; ++i) {
       const int row = (w + NW * i) * RPI + pr;
-      woff[i] = row < t.ncols ? (uint32_t)row * rowb + pc : kOOB;
+      woff[i] = row < t.ncols ? (uint32_t)row * rowb + pc(i) : kOOB;
     }
     if constexpr (!SCREG) {
       xs_r = xs_of(t);
@@ -233,13 +258,15 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   };
   auto issue = [&](int it, int slot) {
     const uint32_t k0 = (uint32_t)it * kRowB;
-    const uint32_t ko = k0 + pc < rowb ? k0 : kPastEnd;
+    uint32_t ko[2];   // by the parity of the transfer
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ko[i] = k0 + pc(i) < rowb ? k0 : kPastEnd;
     char* sb = lds + slot * kStageB;
 #pragma unroll
-    for (int i = 0; i < XI; ++i) dma16(x_r, sb + (w + NW * i) * 1024, xoff[i] + ko);
+    for (int i = 0; i < XI; ++i) dma16(x_r, sb + (w + NW * i) * 1024, xoff[i] + ko[i & 1]);
 #pragma unroll
     for (int i = 0; i < WI; ++i)
-      dma16(w_r, sb + BM * kRowB + (w + NW * i) * 1024, woff[i] + ko);
+      dma16(w_r, sb + BM * kRowB + (w + NW * i) * 1024, woff[i] + ko[i & 1]);
     if constexpr (!SCREG) {
       const uint32_t b0 = (uint32_t)it * 8;
       const uint32_t so = b0 + (lane & 1) * 4 < (uint32_t)sld ? b0 : kPastEnd;
@@ -335,8 +362,40 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   const uint32_t wsc = (uint32_t)(BM + wn * TN * 32 + m) * SRowB + 4 * h;
 
   int slot = 0, cslot = 1;
+  f32x16 acc[TN][TM];
+  u32x4 xo[2][TM], wo[2][TN];   // operands of two steps
+  uint32_t sx[TM], sv[TN];      // scale words of a stage
+  auto read_scales = [&](int it) {
+    if (SCREG && it % 2 == 0) cslot ^= 1;
+    const char* ss = SCREG ? lsc + cslot * kScaleB + it % 2 * 8 : lsc + slot * kScaleB;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) sx[j] = *(const uint32_t*)(ss + xsc + j * 32 * SRowB);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) sv[i] = *(const uint32_t*)(ss + wsc + i * 32 * SRowB);
+    if (it * 8 + 8 > kb) {   // the padding of a scale row is not a scale
+#pragma unroll
+      for (int j = 0; j < TM; ++j) sx[j] = keep_blocks(sx[j], it * 8 + 4 * h, kb);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) sv[i] = keep_blocks(sv[i], it * 8 + 4 * h, kb);
+    }
+  };
+  // step j of the stage in `slot`: chunk 4 h + j of every row, into buffer j % 2
+  auto read = [&](int j) {
+    const char* sb = lds + slot * kStageB + (sw ^ (uint32_t)(j << 4));
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wo[j & 1][i] = *(const u32x4*)(sb + wrow + i * 32 * kRowB);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xo[j & 1][i] = *(const u32x4*)(sb + xrow + i * 32 * kRowB);
+  };
+  auto step = [&](auto jc) {
+    constexpr int J = decltype(jc)::value;
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        acc[i][j] = mfma_mx32<J>(wo[J & 1][i], xo[J & 1][j], acc[i][j], sv[i], sx[j]);
+  };
   for (;;) {
-    f32x16 acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -345,9 +404,9 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
     for (int it = 0; it < kt; ++it) {
-      // this stage is there once at most the transfers of the later ones are
-      // outstanding; then the barrier makes every wave's part visible and
-      // frees the buffer read in the previous iteration
+      // this stage is there once at most the transfers of the later ones
+      // are outstanding; then the barrier makes every wave's part visible
+      // and frees the buffer read in the previous iteration
       constexpr int AH = NST - 2, OPS = XI + WI + SI;
       if (AH > 0 && has_ld)
         __builtin_amdgcn_s_waitcnt(vm_lds(AH * OPS));
@@ -355,45 +414,16 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
         __builtin_amdgcn_s_waitcnt(vm_lds(0));
       barrier_no_fence();
       fetch();
-      if (SCREG && it % 2 == 0) cslot ^= 1;
-      const char* sb = lds + slot * kStageB;
-      const char* ss = SCREG ? lsc + cslot * kScaleB + it % 2 * 8 : lsc + slot * kScaleB;
-      uint32_t sx[TM], sv[TN];
-#pragma unroll
-      for (int j = 0; j < TM; ++j) sx[j] = *(const uint32_t*)(ss + xsc + j * 32 * SRowB);
-#pragma unroll
-      for (int i = 0; i < TN; ++i) sv[i] = *(const uint32_t*)(ss + wsc + i * 32 * SRowB);
-      if (it * 8 + 8 > kb) {   // the padding of a scale row is not a scale
-#pragma unroll
-        for (int j = 0; j < TM; ++j) sx[j] = keep_blocks(sx[j], it * 8 + 4 * h, kb);
-#pragma unroll
-        for (int i = 0; i < TN; ++i) sv[i] = keep_blocks(sv[i], it * 8 + 4 * h, kb);
-      }
-      u32x4 xo[2][TM], wo[2][TN];
-      auto read = [&](int buf, int j) {
-        const uint32_t c = sw ^ (uint32_t)(j << 4);
-#pragma unroll
-        for (int i = 0; i < TN; ++i) wo[buf][i] = *(const u32x4*)(sb + wrow + c + i * 32 * kRowB);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) xo[buf][i] = *(const u32x4*)(sb + xrow + c + i * 32 * kRowB);
-      };
-      auto step = [&](auto jc) {
-        constexpr int J = decltype(jc)::value;
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-          for (int j = 0; j < TM; ++j)
-            acc[i][j] = mfma_mx32<J>(wo[J & 1][i], xo[J & 1][j], acc[i][j], sv[i], sx[j]);
-      };
-      read(0, 0);
-      read(1, 1);
+      read_scales(it);
+      // a step's operand reads go before the products of the step before it
+      read(0);
+      read(1);
       step(std::integral_constant<int, 0>());
-      read(0, 2);
+      read(2);
       step(std::integral_constant<int, 1>());
-      read(1, 3);
+      read(3);
       step(std::integral_constant<int, 2>());
       step(std::integral_constant<int, 3>());
-      // a step's operand reads go before the products of the step before it
       __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
 #pragma unroll
       for (int j = 0; j < 3; ++j) {

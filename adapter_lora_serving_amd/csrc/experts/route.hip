@@ -150,7 +150,8 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     score[threadIdx.x * V + i] = s[i];
-    key[i] = (x[i] == -kInf || b[i] != b[i] || b[i] == -kInf) ? 0u : order_key(b[i]);
+    const float c = x[i] == -kInf ? -kInf : b[i];
+    key[i] = c > -kInf ? order_key(c) : 0u;   // neither NaN nor -inf
   }
 
   if (a.top_groups < a.groups) {
@@ -209,10 +210,17 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
     }
     const uint64_t all = __ballot(l < a.groups && rank < a.top_groups);
     const uint32_t keep = (uint32_t)(all >> (lane_id() & ~(L - 1)));
+    if (gs % V == 0) {   // one group a lane
+      const int grp = (int)(((uint64_t)(uint32_t)e0 * gmagic) >> 21);
+      const bool in = (keep >> (grp & 31)) & 1u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int grp = (int)(((uint64_t)(uint32_t)(e0 + i) * gmagic) >> 21);
-      if (!((keep >> (grp & 31)) & 1u)) key[i] = 0u;
+      for (int i = 0; i < V; ++i) key[i] = in ? key[i] : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int grp = (int)(((uint64_t)(uint32_t)(e0 + i) * gmagic) >> 21);
+        if (!((keep >> (grp & 31)) & 1u)) key[i] = 0u;
+      }
     }
   }
 
@@ -220,18 +228,18 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
   // holds consecutive experts, so the lowest lane that holds the largest key
   // holds the lowest expert of that key.
   for (int r = 0; r < a.k; ++r) {
-    uint32_t best = 0;
-    int bi = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] > best) { best = key[i]; bi = i; }
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
     const uint32_t top = over_lanes<L>(best, umax2);
     const uint64_t eq = __ballot(best == top) >> (lane_id() & ~(L - 1));
     if (l == __ffsll((unsigned long long)eq) - 1) {
+      int bi = V;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) bi = key[i] == top ? i : bi;
       chosen[tok][r] = top ? e0 + bi : -1;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == bi) key[i] = 0u;
+      for (int i = 0; i < V; ++i) key[i] = i == bi ? 0u : key[i];
     }
   }
   // the token's lanes are lanes of one wave, whose LDS operations are in order

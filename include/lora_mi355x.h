@@ -448,7 +448,7 @@ size_t lora_noalloc_scratch_bytes(void);
  *
  * The conventions above hold. Limits checked on the host: 1 <= num_experts
  * <= 1024, 1 <= top_k <= 32, T * top_k < 2^31, rows < 2^31, N and K at most
- * 2^20.
+ * 2^20, and rows * K <= 2^32 for one quantisation.
  *
  * MXFP4 of rows of K values (K a multiple of 32):
  *   codes  [rows, K / 2]  uint8: two 4-bit codes a byte, the even element low.

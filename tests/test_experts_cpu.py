@@ -139,6 +139,7 @@ def test_quantize_refusals(lib):
         return lib.lora_quantize_mxfp4(dtype, form, x, xr, ri, rows, K, ro, c, s, None)
     assert call(dtype=3) == UNSUPPORTED
     assert call(K=(1 << 20) + 32) == UNSUPPORTED
+    assert call(rows=1 << 13, xr=1 << 13, K=1 << 20) == UNSUPPORTED       # 2^33 values
     for kw in (dict(form=3), dict(rows=-1), dict(K=0), dict(xr=-1), dict(x=None), dict(c=None),
                dict(s=None), dict(xr=3), dict(form=1, ro=A16), dict(form=1, ri=A16),
                dict(form=1, ri=A16, ro=A16, xr=0), dict(form=2)):

@@ -270,6 +270,16 @@ def test_quantize_halves_round_to_even():
         check_quantized(L.quantize_mxfp4(d), f64(d))
 
 
+def test_dequantize_every_code_at_every_scale():
+    t = torch()
+    codes = t.arange(256, dtype=t.uint8, device=DEV).repeat(256, 1)      # both halves of a byte
+    scales = t.arange(256, dtype=t.uint8, device=DEV).unsqueeze(1).repeat(1, 16)
+    want = t.from_numpy(X.dequantize(codes.cpu().numpy(), scales.cpu().numpy()))
+    for out in (t.bfloat16, t.float32):
+        v = L.dequantize_mxfp4(L.MXFP4(codes, scales), out)
+        assert np.array_equal(f64(v), want.to(out).double().numpy(), equal_nan=True)
+
+
 def test_quantize_stacked_weights():
     t = torch()
     w = t.randn(3, 40, 96, device=DEV, generator=gen(1))
