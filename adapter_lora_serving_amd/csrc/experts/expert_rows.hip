@@ -31,8 +31,9 @@ __device__ __forceinline__ void put_row(int i, int t, int row, bool live, int sl
 }
 
 // A decode step's few choices over few experts: one wave, no barrier (the
-// one-wave sort of the slot addressing, with the rows written in its place).
-// 512 choices of 8 experts: one launch in place of two.
+// one-wave sort of the slot addressing, with the rows written in its place and
+// their slots asked for with the choices). 512 choices of 8 experts: 4.6 us;
+// the addressing and a second launch took 18 us a call.
 template <int G>
 __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ ids, int n,
                                                   uint32_t kmul, int E, const int32_t* __restrict__ token_slot,
@@ -80,7 +81,8 @@ __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ id
 // all n of them for itself, those before its own apart from the rest, so no
 // workgroup waits for another. The counting reads n ids from L2 a workgroup:
 // 65536 choices are 64 workgroups of 256 KB each; past that the two passes
-// of the addressing count once.
+// of the addressing count once. 65536 choices of 256 experts: 11 us, bound by
+// the LDS adds of the counting (the two passes and the finish: 17 us).
 constexpr int kRowsBlock = 1024;
 constexpr int kRowsOneLaunch = 1 << 16;
 constexpr int kCopies = 4;   // of the counters: neighbouring lanes add to others
@@ -220,7 +222,9 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
 
 // y[t] = residual[t] + sum over j of weights[t, j] * rows[positions[t, j]],
 // j ascending in fp32, rounded once. A position outside [0, nrows) adds
-// nothing. 8 (bf16) or 4 (f32) columns per thread.
+// nothing. 16 bytes of columns per thread, a workgroup a token: the rows'
+// bytes are the time. 8192 tokens x 8 rows x 4096 bf16 onto the residual: 132
+// us for 671 MB, 5.1 TB/s.
 template <typename D>
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ rows, int64_t nrows,
                                                  int H, const int32_t* __restrict__ positions,

@@ -6,12 +6,25 @@
 // "spark_model/lora/expert_apply.rs" (the experts' products on rows sorted
 // by expert, before the experts' LoRA is added to them).
 //
-// v_mfma_scale_f32_16x16x128_f8f6f4 takes 32 codes and a scale byte of each
-// operand per lane: lane (m = lane & 15, g = lane >> 4) supplies row m, block
-// g of 32 of a K step of 128, and receives D[4g + i][m] in element i. The W
-// rows are operand A and the x rows operand B, so a lane ends with 4
-// consecutive columns of one row of y. Products of two 4-bit values and the
-// powers of two are exact; the sums are fp32, y is rounded once.
+// Mathematics: v_mfma_scale_f32_32x32x64_f8f6f4 takes 32 codes and a scale
+// byte of each operand per lane and forms D += A B^T over a K step of 64.
+// Products of two 4-bit values and powers of two are exact; the sums are
+// fp32, in the same order of K in every tile shape, so a row's result does
+// not depend on the batch it is in; y is rounded once. The W rows are operand
+// A and the x rows operand B, so a lane ends with runs of 4 columns of one
+// row of y.
+//
+// What bounds it (MI355X, 4.7 TB/s copy, 2.66 PFLOP/s largest fp8 product):
+//   few rows: the weight's bytes. 512 rows of 8 experts x 28672 x 4096: 113
+//     us, 4.7 TB/s of codes, scales and y.
+//   many rows: 8192 x 28672 x 4096 490 us, 3.9 PFLOP/s; 16384 rows of 8
+//     experts x 4096 x 14336 545 us, 3.5 (its 70 row tiles x 16 take 5 turns
+//     of the 256 units, 4.4 of them full). Of the first one's time the
+//     products alone take 266 us, waiting for their LDS operands 85, for the
+//     transfers 55, scales 20, and the way of y through LDS and out 70.
+//   few tiles (a decode step's dense projections): the walk over K, 0.3 us a
+//     stage of 256. 1 x 6144 x 4096: 8.6 us, of which the launch and the ends
+//     of the walk are 5.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -92,18 +105,19 @@ __device__ __forceinline__ void zero_dead_rows(const MxArgs& a) {
   }
 }
 
-// Row tiles of BM rows over all experts, counted by every wave for itself (no
-// barrier, so that waves may call it at different times).
+// Row tiles of BM rows over all experts, counted by every wave for itself. No
+// more than bounds in order can give, whatever the bounds are.
 template <int BM>
 __device__ __forceinline__ int count_tiles(const MxArgs& a) {
+  const int most = (a.rows + BM - 1) / BM + a.E;
   int tiles = 0;
   for (int s = lane_id(); s < a.E; s += kWave) {
     int beg, len;
     segment_of(a.offsets, s, a.rows, beg, len);
-    tiles += (len + BM - 1) / BM;
+    tiles = min(tiles + (len + BM - 1) / BM, most);
   }
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) tiles += __shfl_xor(tiles, d);
+  for (int d = 1; d < kWave; d <<= 1) tiles = min(tiles + __shfl_xor(tiles, d), most);
   return __builtin_amdgcn_readfirstlane(tiles);
 }
 
@@ -121,7 +135,9 @@ __device__ __forceinline__ void find_tile(const MxArgs& a, int item, int& row, i
     const uint64_t past = __ballot(upto > item);
     if (past != 0) {
       const int src = __ffsll((unsigned long long)past) - 1;
-      const int local = item - (__shfl(upto, src) - __shfl(tiles, src));
+      // within the segment, whatever the bounds are
+      const int mine = __shfl(tiles, src);
+      const int local = max(min(item - (__shfl(upto, src) - mine), mine - 1), 0);
       row = __builtin_amdgcn_readfirstlane(__shfl(beg, src) + local * BM);
       rows = __builtin_amdgcn_readfirstlane(min(BM, __shfl(len, src) - local * BM));
       e = __builtin_amdgcn_readfirstlane(s0 + src);
@@ -131,9 +147,11 @@ __device__ __forceinline__ void find_tile(const MxArgs& a, int item, int& row, i
   }
 }
 
-// LDS of a tile kernel (stages, scale slots), and the workgroups of
-// it that a compute unit's 160 KB hold (at most 16 waves of them: with more,
-// fewer registers a wave than its accumulators and operands need)
+// LDS of a tile kernel (stages, scale slots), and the workgroups of it that a
+// compute unit's 160 KB hold (at most 16 waves of them: with more, fewer
+// registers a wave than its accumulators and operands need). The compiler is
+// held to that many: with 20 registers more the 128 x 128 tile has one
+// workgroup a unit, and the 512-row product above takes 158 us.
 template <int BM, int BN, int NW, int NST, bool SCREG>
 constexpr int lds_bytes() {
   constexpr int SRowB = SCREG ? 16 : 8;
@@ -146,9 +164,11 @@ constexpr int occupancy() {
 }
 
 // BM x BN tiles of y, by a workgroup of WM x WN waves that walks its share of
-// them. K passes in stages of 256 through a ring of NST LDS stages; the ring
-// runs on from one tile into the next, so a tile's first stage is on its way
-// while the tile before it is finished and stored.
+// them. K passes in stages of 256 (whole 128-byte lines of codes; stages of 128
+// in a deeper ring: 700 us against 640 for 8192 x 28672 x 4096) through a ring
+// of NST LDS stages; the ring runs on from one tile into the next, so a tile's
+// first stage is on its way while the tile before it is finished and stored
+// (a workgroup a tile: 590 us against 515).
 template <typename D, int BM, int BN, int WM, int WN, int NST, bool SCREG>
 __global__ __launch_bounds__(64 * WM * WN, ((occupancy<BM, BN, WM * WN, NST, SCREG>() * WM * WN + 3) / 4)) void
 k_mx_tile(MxArgs a, int sld, int ntiles) {
@@ -171,7 +191,7 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   const int w = wave_id();
   const uint32_t rowb = (uint32_t)a.K / 2;
   const int kb = a.K / 32;
-  const int kt = (a.K + kStageK - 1) / kStageK;   // at least NST - 1
+  const int kt = (a.K + kStageK - 1) / kStageK;   // at least NST - 1 (the walk looks one tile ahead)
 
   // the experts' row tiles; rows of no expert become zero
   int mtiles = (a.rows + BM - 1) / BM;
@@ -280,7 +300,8 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   // Scales by way of registers: a group is 64 bytes (K of 2048) of every row,
   // read by 4 lanes side by side so that a line is asked for once, and handed
   // to LDS a chunk at a time by the lanes that hold it. The same bytes by
-  // stage-wise transfers would ask L2 for every line many times.
+  // stage-wise transfers would ask L2 for every line many times: 512 rows of 8
+  // experts x 4096 x 14336 82 us against 106 in 64 x 64 tiles.
   const int piece = lane & 3;
   u32x4 sreg[SCREG ? SI : 1];
   auto load_scales = [&](const Tile& t, int grp) {
@@ -440,7 +461,9 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
     __builtin_amdgcn_sched_barrier(0);
     // The tile goes to memory through the LDS stage just read, so that a
     // store takes whole lines of y: 16 bytes a lane, a row's lanes side by
-    // side. 16-byte chunks of a row are held at chunk ^ (row & 31), so that
+    // side (8 bytes a lane to 32 rows at a time straight from the registers
+    // took 660 us in place of 600 for 8192 x 28672 x 4096, and 49 in place of
+    // 24 where y is float32 with an odd width). 16-byte chunks of a row are held at chunk ^ (row & 31), so that
     // neither the 32 rows a wave writes at a time nor the row it reads meets
     // a bank twice.
     constexpr int kElem = D::kBytes;

@@ -14,7 +14,16 @@
 // The softmax's sum is formed in fp64 and rounded to fp32 once: the fp64
 // sum of at most 1024 fp32 terms is so near the true one that its rounding
 // does not depend on the order, so neither do the scores and the choice
-// between two near experts.
+// between two near experts. The same holds for a sigmoid, which is one
+// expression per expert.
+//
+// What bounds it: issued instructions, not bytes. 8192 tokens x 256 experts,
+// top-8 of 4 of 8 groups, fp32: 9.2 us for 8.9 MB (1.9 us at the copy rate);
+// the rounds of the top-k are about half of it. 16 lanes hold a token of up
+// to 256 experts, so that the reductions stay in a row of lanes (DPP; by way
+// of LDS shuffles with a wave's 64 lanes a row the same took 19 us) and a
+// wave does 4 tokens at a time; 64 lanes hold it past that. One token of 64
+// experts: 2.4 us on the GPU, the least that a launch takes.
 #include "lora_common.h"
 #include "experts.h"
 
