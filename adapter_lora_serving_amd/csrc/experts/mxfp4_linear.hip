@@ -17,11 +17,11 @@
 // What bounds it (MI355X, 4.7 TB/s copy, 2.66 PFLOP/s largest fp8 product):
 //   few rows: the weight's bytes. 512 rows of 8 experts x 28672 x 4096: 113
 //     us, 4.7 TB/s of codes, scales and y.
-//   many rows: 8192 x 28672 x 4096 490 us, 3.9 PFLOP/s; 16384 rows of 8
-//     experts x 4096 x 14336 545 us, 3.5 (its 70 row tiles x 16 take 5 turns
-//     of the 256 units, 4.4 of them full). Of the first one's time the
-//     products alone take 266 us, waiting for their LDS operands 85, for the
-//     transfers 55, scales 20, and the way of y through LDS and out 70.
+//   many rows: 8192 x 28672 x 4096 511 us, 3.8 PFLOP/s; 16384 rows of 8
+//     experts x 4096 x 14336 543 us, 3.5 (its 70 row tiles x 16 take 4.5 turns
+//     of the 256 units). Of the first one's time the products alone take 266
+//     us, waiting for their LDS operands 85, for the transfers 55, scales 20,
+//     and the way of y through LDS and out 70.
 //   few tiles (a decode step's dense projections): the walk over K, 0.3 us a
 //     stage of 256. 1 x 6144 x 4096: 8.6 us, of which the launch and the ends
 //     of the walk are 5.
@@ -206,7 +206,20 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   const int G = mtiles * ntiles;
   const int per = (G + 7) / 8;
   const int stride = (int)gridDim.x >> 3;
-  const int end = min(G - ((int)blockIdx.x & 7) * per, per);   // positions of this XCD
+  int end = min(G - ((int)blockIdx.x & 7) * per, per);   // positions of this XCD
+  // Where the last turn of the XCD's workgroups has tiles for half of them at
+  // most, it has half tiles (BN / 2 columns) for twice as many; the waves of the
+  // other columns, one on every SIMD, only fetch and wait. 16384 rows of 8
+  // experts x 4096 x 14336, whose last turn is 4 tenths full: 543 us in place
+  // of 551; 4262 rows of 9 experts x 6521 x 6496: 181 in place of 196; 8192 x
+  // 28672 x 4096, whose turns are full: 511 in place of 508.
+  constexpr bool HALVES = BN == 256 && WN == 2;
+  static_assert(!HALVES || NST == 2, "a half tile has fewer transfers than the waits count");
+  int halves = end;                                       // the first position with a half tile
+  if (HALVES && end > stride && end % stride * 2 <= stride) {
+    halves = end / stride * stride;
+    end += end - halves;
+  }
   int pos = (int)blockIdx.x >> 3;
   if (pos >= end) return;
   struct Tile {
@@ -214,7 +227,8 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   };
   auto locate = [&](int p) {
     constexpr int kGroupM = 8;
-    const int L = ((int)blockIdx.x & 7) * per + p;
+    const bool half = HALVES && p >= halves;
+    const int L = ((int)blockIdx.x & 7) * per + (half ? halves + (p - halves) / 2 : p);
     const int grp = L / (kGroupM * ntiles);
     const int gsz = min(kGroupM, mtiles - grp * kGroupM);
     const int li = L - grp * kGroupM * ntiles;
@@ -222,6 +236,10 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
     Tile t;
     t.n0 = li / gsz * BN;
     t.ncols = min(BN, a.N - t.n0);
+    if (half) {
+      t.n0 += (p - halves) % 2 * (BN / 2);
+      t.ncols = max(min(BN / 2, a.N - t.n0), 0);
+    }
     t.e = 0;
     t.row = tm * BM;
     t.mrows = min(BM, a.rows - t.row);
@@ -251,7 +269,9 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   auto pc = [&](int i) { return (uint32_t)((lane & 7) ^ swz((w + NW * i) * RPI + pr)) * 16u; };
   uint32_t xoff[XI], woff[WI], soff[SCREG ? 1 : SI];
   rsrc_t xs_r, ws_r;
+  int ld_cols = BN;   // columns of the tile being fetched
   auto point_at = [&](const Tile& t) {
+    ld_cols = t.ncols;
     x_r = make_rsrc(a.x + (int64_t)t.row * rowb, (uint32_t)t.mrows * rowb);
     w_r = make_rsrc(a.w + ((int64_t)t.e * a.N + t.n0) * rowb, (uint32_t)t.ncols * rowb);
 #pragma unroll
@@ -286,7 +306,8 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
     for (int i = 0; i < XI; ++i) dma16(x_r, sb + (w + NW * i) * 1024, xoff[i] + ko[i & 1]);
 #pragma unroll
     for (int i = 0; i < WI; ++i)
-      dma16(w_r, sb + BM * kRowB + (w + NW * i) * 1024, woff[i] + ko[i & 1]);
+      if (!HALVES || (w + NW * i) * RPI < ld_cols)
+        dma16(w_r, sb + BM * kRowB + (w + NW * i) * 1024, woff[i] + ko[i & 1]);
     if constexpr (!SCREG) {
       const uint32_t b0 = (uint32_t)it * 8;
       const uint32_t so = b0 + (lane & 1) * 4 < (uint32_t)sld ? b0 : kPastEnd;
@@ -387,7 +408,6 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   u32x4 xo[2][TM], wo[2][TN];   // operands of two steps
   uint32_t sx[TM], sv[TN];      // scale words of a stage
   auto read_scales = [&](int it) {
-    if (SCREG && it % 2 == 0) cslot ^= 1;
     const char* ss = SCREG ? lsc + cslot * kScaleB + it % 2 * 8 : lsc + slot * kScaleB;
 #pragma unroll
     for (int j = 0; j < TM; ++j) sx[j] = *(const uint32_t*)(ss + xsc + j * 32 * SRowB);
@@ -435,23 +455,26 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
         __builtin_amdgcn_s_waitcnt(vm_lds(0));
       barrier_no_fence();
       fetch();
-      read_scales(it);
-      // a step's operand reads go before the products of the step before it
-      read(0);
-      read(1);
-      step(std::integral_constant<int, 0>());
-      read(2);
-      step(std::integral_constant<int, 1>());
-      read(3);
-      step(std::integral_constant<int, 2>());
-      step(std::integral_constant<int, 3>());
-      __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
+      if (SCREG && it % 2 == 0) cslot ^= 1;
+      if (!HALVES || wn * TN * 32 < cur.ncols) {
+        read_scales(it);
+        // a step's operand reads go before the products of the step before it
+        read(0);
+        read(1);
+        step(std::integral_constant<int, 0>());
+        read(2);
+        step(std::integral_constant<int, 1>());
+        read(3);
+        step(std::integral_constant<int, 2>());
+        step(std::integral_constant<int, 3>());
         __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x100, TN + TM, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, TN * TM, 0);
+        }
         __builtin_amdgcn_sched_group_barrier(0x008, TN * TM, 0);
       }
-      __builtin_amdgcn_sched_group_barrier(0x008, TN * TM, 0);
       if (it + 1 < kt) slot = slot + 1 == NST ? 0 : slot + 1;
     }
 

@@ -423,6 +423,28 @@ def test_linear_same_bits_every_time_and_in_every_tiling():
         assert t.equal(part, y[lo:hi, :cols])
 
 
+@pytest.mark.parametrize("rows,N", [(5120, 3840), (4910, 3740), (5000, 3700)])
+def test_linear_half_tiles(rows, N):
+    """Some 300 tiles of 256 x 256, the last ones as halves: the second half of
+    the last columns is whole, 28 columns and nothing."""
+    x, w = held(rows, 544, rows), held(N, 544, N)
+    check_product(L.mxfp4_linear(x, w, dtype=torch().float32), values(x), values(w), 544)
+
+
+def test_expert_linear_half_tiles():
+    t = torch()
+    rows, E, N, K = 3900, 4, 4700, 544   # 19 tiles of columns and 17 or so of rows
+    x = held(rows, K, 3)
+    W = L.MXFP4(*(v.view(E, N, -1) for v in held(E * N, K, E)))
+    off = [7, 1300, 1301, 2600, 3890]
+    y = L.mxfp4_expert_linear(x, W, t.tensor(off, dtype=t.int32, device=DEV))
+    xv = values(x)
+    assert bool((y[:7] == 0).all()) and bool((y[3890:] == 0).all())
+    for e in range(E):
+        check_product(y[off[e]:off[e + 1]], xv[off[e]:off[e + 1]],
+                      values(L.MXFP4(W.codes[e], W.scales[e])), K, f"expert {e}")
+
+
 @pytest.mark.parametrize("bounds", [
     [0, 0, 5, 5, 40, 40], [0, 70, 70, 70, 70, 70], [3, 10, 10, 30, 31, 60], [0, 0, 0, 0, 0, 0],
     [0, 1, 2, 3, 4, 70], [70, 70, 70, 70, 70, 70]])
