@@ -18,12 +18,13 @@
 // expression per expert.
 //
 // What bounds it: issued instructions, not bytes. 8192 tokens x 256 experts,
-// top-8 of 4 of 8 groups, fp32: 9.2 us for 8.9 MB (1.9 us at the copy rate);
-// the rounds of the top-k are about half of it. 16 lanes hold a token of up
-// to 256 experts, so that the reductions stay in a row of lanes (DPP; by way
+// top-8 of 4 of 8 groups, fp32: 8.1 us for 8.9 MB (1.9 us at the copy rate),
+// of which 0.25 us a round of the top-k, 1.1 the groups. 16 lanes hold a token
+// of up to 256 experts, so that the reductions stay in a row of lanes (DPP; by way
 // of LDS shuffles with a wave's 64 lanes a row the same took 19 us) and a
 // wave does 4 tokens at a time; 64 lanes hold it past that. One token of 64
 // experts: 2.4 us on the GPU, the least that a launch takes.
+#include <type_traits>
 #include "lora_common.h"
 #include "experts.h"
 
@@ -39,10 +40,16 @@ __device__ __forceinline__ uint32_t order_key(float c) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// v of the lane N places on in its row of 16 lanes (a rotation).
+// v of the lane N places before in its row of 16 lanes (a rotation). Every
+// lane has a source, so the old value and the bound never count; as 0 and
+// true they let the compiler fold the move into the operation on it.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
 template <int N>
 __device__ __forceinline__ uint32_t ror(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 | N, 0xf, 0xf, false);
+  return dpp<0x120 | N>(v);
 }
 template <int N>
 __device__ __forceinline__ float ror(float v) {
@@ -66,6 +73,42 @@ __device__ __forceinline__ T over_lanes(T v, Op op) {
     v = op(v, __shfl_xor(v, 32));
   }
   return v;
+}
+
+// b0 >= b1 become the two largest of b0, b1 and k; b1 their median.
+__device__ __forceinline__ void two_largest(uint32_t& b0, uint32_t& b1, uint32_t k) {
+  b1 = max(min(b0, b1), min(max(b0, b1), k));
+  b0 = max(b0, k);
+}
+
+// The two largest of the keys of `per` (1 to 16, a power of two) lanes side by
+// side, from each lane's two largest, in all of them: lanes 1 and 2 apart, then
+// the mirrors of 8 and of 16 lanes, whose halves hold the same by then.
+__device__ __forceinline__ void best_two(uint32_t& b0, uint32_t& b1, int per) {
+  auto merge = [&](uint32_t o0, uint32_t o1) {
+    b1 = max(max(b1, o1), min(b0, o0));
+    b0 = max(b0, o0);
+  };
+  if (per >= 2) merge(dpp<0xb1>(b0), dpp<0xb1>(b1));
+  if (per >= 4) merge(dpp<0x4e>(b0), dpp<0x4e>(b1));
+  if (per >= 8) merge(dpp<0x141>(b0), dpp<0x141>(b1));
+  if (per >= 16) merge(dpp<0x140>(b0), dpp<0x140>(b1));
+}
+
+// Is this lane the first of its token's L lanes with `is`? One of them has it.
+template <int L>
+__device__ __forceinline__ bool first_of(bool is, int l) {
+  const uint64_t all = __ballot(is) >> (lane_id() & ~(L - 1));
+  return l == (L <= 32 ? __builtin_ctz((uint32_t)all) : __builtin_ctzll(all));
+}
+
+// f(N) for N from 1 to 15, as constants.
+template <int N = 1, typename F>
+__device__ __forceinline__ void for_rotations(F f) {
+  if constexpr (N < 16) {
+    f(std::integral_constant<int, N>());
+    for_rotations<N + 1>(f);
+  }
 }
 
 // The choice score that an order key stands for.
@@ -109,9 +152,10 @@ __device__ __forceinline__ void load_row(const T* row, int e0, int E, float* x) 
 template <typename T, int L, int V>
 __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
                                                const float* __restrict__ bias, RouteArgs a,
-                                               uint32_t gmagic, int32_t* __restrict__ ids,
+                                               int gs, uint32_t gmagic, int32_t* __restrict__ ids,
                                                float* __restrict__ weights) {
   __shared__ __attribute__((aligned(16))) float score[256 * V];
+  __shared__ u32x4 held[V >= 8 ? V / 4 : 1][256];
   __shared__ int chosen[256 / L][kMaxTopK];
   const int l = threadIdx.x % L;
   const int tok = threadIdx.x / L;
@@ -164,67 +208,65 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
   }
 
   if (a.top_groups < a.groups) {
-    // lane g of the token's lanes keeps the worth of group g, then its rank
-    // among the groups says whether it stays
-    float worth = -kInf;
-    const int gs = a.E / a.groups;
     auto worth_of = [&](uint32_t b0, uint32_t b1) {
       const float v = b0 ? key_value(b0) : -kInf;
       return a.sum2 && b1 ? v + key_value(b1) : v;
     };
-    if (gs % V == 0) {
-      // every lane's experts are of one group, gs / V lanes side by side hold
-      // it: two best of the lane, then of the group's lanes
+    // `per` lanes side by side hold the worth of a group, those past the groups
+    // -inf. Where the lanes of a group are whole and a power of two they are
+    // those of its experts; else lane g stands for group g, whose experts are
+    // looked for in every lane (8192 x 256, 8 groups: 8.1 us against 11.3).
+    const bool whole = gs % V == 0 && gs / V <= 16 && (gs / V & (gs / V - 1)) == 0;
+    const int per = whole ? gs / V : 1;
+    float worth = -kInf;
+    if (whole) {
       uint32_t b0 = 0, b1 = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        b1 = max(b1, min(b0, key[i]));
-        b0 = max(b0, key[i]);
+        two_largest(b0, b1, key[i]);
       }
-      const int per = gs / V;
-      const int first = l / per * per;
-      uint32_t g0 = 0, g1 = 0;
-      for (int q = 0; q < per; ++q) {
-        const int src = min(first + q, L - 1);
-        const uint32_t o0 = (uint32_t)__shfl((int)b0, src, L);
-        const uint32_t o1 = (uint32_t)__shfl((int)b1, src, L);
-        g1 = max(max(g1, o1), min(g0, o0));
-        g0 = max(g0, o0);
-      }
-      worth = __shfl(worth_of(g0, g1), min(l * per, L - 1), L);
-      if (l >= a.groups) worth = -kInf;
+      best_two(b0, b1, per);
+      worth = worth_of(b0, b1);
     } else {
       for (int g = 0; g < a.groups; ++g) {
         uint32_t b0 = 0, b1 = 0;   // two best keys of the group
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int grp = (int)(((uint64_t)(uint32_t)(e0 + i) * gmagic) >> 21);
-          const uint32_t q = grp == g ? key[i] : 0u;
-          b1 = max(b1, min(b0, q));
-          b0 = max(b0, q);
+          two_largest(b0, b1, grp == g ? key[i] : 0u);
         }
         // the second best is the best but one lane's best, or that lane's second
         const uint32_t top = over_lanes<L>(b0, umax2);
-        const uint64_t eq = __ballot(b0 == top) >> (lane_id() & ~(L - 1));
-        const bool mine = l == __ffsll((unsigned long long)eq) - 1;
-        const uint32_t sec = over_lanes<L>(mine ? b1 : b0, umax2);
+        const uint32_t sec = over_lanes<L>(first_of<L>(b0 == top, l) ? b1 : b0, umax2);
         const float wv = worth_of(top, sec);
         if (l == g) worth = wv;
       }
     }
+    // the lanes of better groups, of equal ones the lanes before
+    const int first = l & -per;
     int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const float o = __shfl(worth, g, L);
-      rank += (o > worth || (o == worth && g < l)) ? 1 : 0;
+    if constexpr (L == 16) {
+      for_rotations([&](auto n) {
+        constexpr int N = decltype(n)::value;
+        const float o = ror<N>(worth);
+        rank += (int)(o > worth) | ((int)(o == worth) & (int)(l >= N));   // no branches
+      });
+      rank -= l - first;   // its own lanes before it
+    } else {
+      for (int g = 0; g < a.groups; ++g) {   // a wave a token
+        const float o = __uint_as_float(
+            (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(worth), g * per));
+        rank += (int)(o > worth) | ((int)(o == worth) & (int)(g * per < first));
+      }
+      rank *= per;
     }
-    const uint64_t all = __ballot(l < a.groups && rank < a.top_groups);
-    const uint32_t keep = (uint32_t)(all >> (lane_id() & ~(L - 1)));
-    if (gs % V == 0) {   // one group a lane
-      const int grp = (int)(((uint64_t)(uint32_t)e0 * gmagic) >> 21);
-      const bool in = (keep >> (grp & 31)) & 1u;
+    const bool in = rank < a.top_groups * per;
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = in ? key[i] : 0u;
     } else {
+      const uint32_t keep =
+          (uint32_t)(__ballot(in && l < a.groups) >> (lane_id() & ~(L - 1)));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int grp = (int)(((uint64_t)(uint32_t)(e0 + i) * gmagic) >> 21);
@@ -235,20 +277,55 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
 
   // top_k rounds: the largest key, its lowest expert, out with it. A lane
   // holds consecutive experts, so the lowest lane that holds the largest key
-  // holds the lowest expert of that key.
-  for (int r = 0; r < a.k; ++r) {
-    uint32_t best = key[0];
+  // holds the lowest expert of that key. From 8 experts a lane on it holds the
+  // best of each 4 of its keys in registers and the keys in LDS, and only the
+  // 4 that lose one are looked at again (32768 x 256, top-8 without groups:
+  // 17.2 us; all keys in registers, every one compared and masked a round: 20.1;
+  // with 128 experts 11.1 and 12.6).
+  if constexpr (V >= 8) {
+    constexpr int NQ = V / 4;
+    uint32_t best4[NQ];
 #pragma unroll
-    for (int i = 1; i < V; ++i) best = max(best, key[i]);
-    const uint32_t top = over_lanes<L>(best, umax2);
-    const uint64_t eq = __ballot(best == top) >> (lane_id() & ~(L - 1));
-    if (l == __ffsll((unsigned long long)eq) - 1) {
-      int bi = V;
+    for (int q = 0; q < NQ; ++q) {
+      best4[q] = max(max(key[4 * q], key[4 * q + 1]), max(key[4 * q + 2], key[4 * q + 3]));
+      held[q][threadIdx.x] = u32x4{key[4 * q], key[4 * q + 1], key[4 * q + 2], key[4 * q + 3]};
+    }
+    for (int r = 0; r < a.k; ++r) {
+      uint32_t best = best4[0];
 #pragma unroll
-      for (int i = V - 1; i >= 0; --i) bi = key[i] == top ? i : bi;
-      chosen[tok][r] = top ? e0 + bi : -1;
+      for (int q = 1; q < NQ; ++q) best = max(best, best4[q]);
+      const uint32_t top = over_lanes<L>(best, umax2);
+      if (first_of<L>(best == top, l)) {
+        int q = NQ - 1;
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = i == bi ? 0u : key[i];
+        for (int i = NQ - 2; i >= 0; --i) q = best4[i] == top ? i : q;
+        u32x4 v = held[q][threadIdx.x];
+        const int bi = v.x == top ? 0 : v.y == top ? 1 : v.z == top ? 2 : 3;
+        chosen[tok][r] = top ? e0 + 4 * q + bi : -1;
+        v.x = bi == 0 ? 0u : v.x;
+        v.y = bi == 1 ? 0u : v.y;
+        v.z = bi == 2 ? 0u : v.z;
+        v.w = bi == 3 ? 0u : v.w;
+        held[q][threadIdx.x] = v;
+        const uint32_t left = max(max(v.x, v.y), max(v.z, v.w));
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) best4[i] = i == q ? left : best4[i];
+      }
+    }
+  } else {
+    for (int r = 0; r < a.k; ++r) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = max(best, key[i]);
+      const uint32_t top = over_lanes<L>(best, umax2);
+      if (first_of<L>(best == top, l)) {
+        int bi = V;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i) bi = key[i] == top ? i : bi;
+        chosen[tok][r] = top ? e0 + bi : -1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = i == bi ? 0u : key[i];
+      }
     }
   }
   // the token's lanes are lanes of one wave, whose LDS operations are in order
@@ -276,11 +353,11 @@ hipError_t launch_route_experts(int dtype, const void* logits, const float* bias
                                 hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   // e / (E / groups) as a product: exact for e < 1024 and group sizes <= 1024
-  const uint32_t gs = (uint32_t)(a.E / a.groups);
-  const uint32_t gmagic = (1u << 21) / gs + 1u;
+  const int gs = a.E / a.groups;
+  const uint32_t gmagic = (1u << 21) / (uint32_t)gs + 1u;
 #define LAUNCH(TT, LV, VV)                                                                     \
   hipLaunchKernelGGL((k_route<TT, LV, VV>), dim3((unsigned)((a.T + 256 / LV - 1) / (256 / LV))), \
-                     dim3(256), 0, stream, (const TT*)logits, bias, a, gmagic, ids, weights)
+                     dim3(256), 0, stream, (const TT*)logits, bias, a, gs, gmagic, ids, weights)
 #define BY_E(TT)                              \
   do {                                        \
     if (a.E <= 16) LAUNCH(TT, 16, 1);         \
