@@ -81,19 +81,24 @@ __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ id
 // all n of them for itself, those before its own apart from the rest, so no
 // workgroup waits for another. The counting reads n ids from L2 a workgroup:
 // 65536 choices are 64 workgroups of 256 KB each; past that the two passes
-// of the addressing count once. 65536 choices of 256 experts: 11 us, bound by
-// the LDS adds of the counting (the two passes and the finish: 17 us).
+// of the addressing count once. 65536 choices of 256 experts: 10.4 us, bound by
+// the instructions and LDS adds of the counting (the two passes and the finish:
+// 17 us). Neighbouring lanes add to other copies of the counters, since lanes
+// that add to one address wait for each other: 4, 8 and 16 copies take 10.2,
+// 10.2 and 10.4 us where the choices are spread evenly, 18.8, 12.1 and 9.5
+// where all are of one expert (or dead). 16 fit the LDS up to 512 experts.
 constexpr int kRowsBlock = 1024;
 constexpr int kRowsOneLaunch = 1 << 16;
-constexpr int kCopies = 4;   // of the counters: neighbouring lanes add to others
 
+template <int kCopies>
 __global__ __launch_bounds__(kRowsBlock) void k_rows_block(
     const int32_t* __restrict__ ids, int n, uint32_t kmul, int E,
-    const int32_t* __restrict__ token_slot, int32_t* __restrict__ row_token, int32_t* __restrict__ positions,
-    int32_t* __restrict__ offsets, int32_t* __restrict__ row_slot) {
+    const int32_t* __restrict__ token_slot, int32_t* __restrict__ row_token,
+    int32_t* __restrict__ positions, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ row_slot) {
   extern __shared__ int smem[];
   const int S1 = E + 1;
-  int* cnt = smem;               // [16][S1] per-wave counts, then offsets in the workgroup
+  int* cnt = smem;                    // [16][S1] per-wave counts, then offsets in the workgroup
   int* before = cnt + 16 * S1;        // [kCopies][S1] choices before this workgroup's
   int* rest = before + kCopies * S1;  // [kCopies][S1] the others
   int* scratch = rest + kCopies * S1; // [20]
@@ -108,23 +113,26 @@ __global__ __launch_bounds__(kRowsBlock) void k_rows_block(
   const int slot = row_slot && i0 < n ? token_slot[t0] : -1;
   __syncthreads();
   if (g.leader) cnt[w * S1 + g.key] += g.count;   // distinct keys: no collision
-  auto count = [&](int i, int id) {
-    const int key = id >= 0 && id < E ? id : E;
-    atomicAdd((i < own0 ? before : rest) + tid % kCopies * S1 + key, 1);
-  };
-  // whole vectors from the first 16-byte boundary on, single ids around them
-  const int head = min(n, (int)(-(reinterpret_cast<intptr_t>(ids) >> 2) & 3));
-  const int tail = head + ((n - head) & ~3);
+  // ids [lo, hi) into a histogram: whole vectors from the first 16-byte
+  // boundary on, single ids around them
+  auto count = [&](int lo, int hi, int* hist) {
+    hist += tid % kCopies * S1;
+    auto add = [&](uint32_t id) { atomicAdd(hist + min(id, (uint32_t)E), 1); };
+    const int head = min(hi, lo + (int)(-(reinterpret_cast<intptr_t>(ids + lo) >> 2) & 3));
+    const int tail = head + ((hi - head) & ~3);
 #pragma unroll 4
-  for (int i = head + tid * 4; i < tail; i += kRowsBlock * 4) {
-    const u32x4 v = *(const u32x4*)(ids + i);
-    count(i, (int)v.x);
-    count(i + 1, (int)v.y);
-    count(i + 2, (int)v.z);
-    count(i + 3, (int)v.w);
-  }
-  if (tid < head) count(tid, ids[tid]);
-  if (tail + tid < n) count(tail + tid, ids[tail + tid]);
+    for (int i = head + tid * 4; i < tail; i += kRowsBlock * 4) {
+      const u32x4 v = *(const u32x4*)(ids + i);
+      add(v.x);
+      add(v.y);
+      add(v.z);
+      add(v.w);
+    }
+    if (lo + tid < head) add((uint32_t)ids[lo + tid]);
+    if (tail + tid < hi) add((uint32_t)ids[tail + tid]);
+  };
+  count(0, min(own0, n), before);
+  count(min(own0, n), n, rest);
   __syncthreads();
   int tot = 0;   // key tid (S1 <= 1025: the last key by thread 0 below)
   auto offsets_of = [&](int key) {
@@ -188,9 +196,8 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
   const uint32_t kmul = k == 1 ? 0u : (uint32_t)(((1ull << 32) + k - 1) / k);
   if (n <= 16 * kWave && E < kWave) {
 #define W(GV)                                                                              \
-  hipLaunchKernelGGL(k_rows_wave<GV>, dim3(1), dim3(kWave), 0, stream, ids, n, kmul, E,          \
-                     token_slot, \
-                     row_token, positions, offsets, row_slot)
+  hipLaunchKernelGGL(k_rows_wave<GV>, dim3(1), dim3(kWave), 0, stream, ids, n, kmul, E,    \
+                     token_slot, row_token, positions, offsets, row_slot)
     const int groups = (n + kWave - 1) / kWave;
     if (groups <= 1) W(1);
     else if (groups <= 2) W(2);
@@ -202,14 +209,16 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
   }
   if (n <= kRowsOneLaunch) {
     const int nb = n == 0 ? 1 : (n + kRowsBlock - 1) / kRowsBlock;
-    const size_t lds = ((size_t)(16 + 2 * kCopies) * (E + 1) + 20) * sizeof(int);
+    const int copies = E <= 512 ? 16 : 8;
+    auto* const f = copies == 16 ? k_rows_block<16> : k_rows_block<8>;
+    const size_t lds = ((size_t)(16 + 2 * copies) * (E + 1) + 20) * sizeof(int);
     if (lds > 65536) {
-      const hipError_t e = hipFuncSetAttribute((const void*)k_rows_block,
+      const hipError_t e = hipFuncSetAttribute((const void*)f,
                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k_rows_block, dim3(nb), dim3(kRowsBlock), lds, stream, ids, n, kmul, E,
-                       token_slot, row_token, positions, offsets, row_slot);
+    hipLaunchKernelGGL(f, dim3(nb), dim3(kRowsBlock), lds, stream, ids, n, kmul, E, token_slot,
+                       row_token, positions, offsets, row_slot);
     return hipGetLastError();
   }
   hipError_t e = launch_build_addressing(ids, n, E, row_token, offsets, ws,
