@@ -147,6 +147,26 @@ __device__ __forceinline__ void find_tile(const MxArgs& a, int item, int& row, i
   }
 }
 
+// The scales in LDS: a ring of groups, each the next kRowB bytes of every
+// row's. By way of registers a group serves two stages. By transfers it is a
+// stage's own 8 bytes of a row, or in 64 x 128 tiles those of 4 stages, with
+// the first of them, which asks for a line a quarter as often: 256 x 6144 x
+// 4096 12.7 us against 15.4, 16 x 28672 x 4096 16.1 against 18.9. In 64 x 64
+// tiles, which have fewer rows to a wave, 128 x 4096 x 4096 takes 9.1 us that
+// way against 8.8.
+template <int BM, int BN, int NW, int NST, bool SCREG>
+struct Scales {
+  static constexpr int kRowB = SCREG ? 16 : NST > 2 && BM < BN ? 32 : 8;
+  static constexpr int kStages = kRowB / 8;                        // that a group serves
+  static constexpr int kRows = 256 / kRowB;                        // of a wave's operation
+  static constexpr int kOps = ((BM + BN) / kRows + NW - 1) / NW;   // of a wave and group
+  static constexpr int kSlotB = kOps * NW * 256;
+  // The NST stages read and on their way are of as many groups at most where a
+  // group is a stage, else of 3: a tile has NST - 1 stages at least, so only
+  // its last group can be of one.
+  static constexpr int kSlots = kStages == 1 || NST < 3 ? NST : 3;
+};
+
 // LDS of a tile kernel (stages, scale slots), and the workgroups of it that a
 // compute unit's 160 KB hold (at most 16 waves of them: with more, fewer
 // registers a wave than its accumulators and operands need). The compiler is
@@ -154,8 +174,8 @@ __device__ __forceinline__ void find_tile(const MxArgs& a, int item, int& row, i
 // workgroup a unit, and the 512-row product above takes 158 us.
 template <int BM, int BN, int NW, int NST, bool SCREG>
 constexpr int lds_bytes() {
-  constexpr int SRowB = SCREG ? 16 : 8;
-  return NST * ((BM + BN) * kRowB + ((BM + BN) * SRowB / 256 + NW - 1) / NW * NW * 256);
+  using S = Scales<BM, BN, NW, NST, SCREG>;
+  return NST * (BM + BN) * kRowB + S::kSlots * S::kSlotB;
 }
 template <int BM, int BN, int NW, int NST, bool SCREG>
 constexpr int occupancy() {
@@ -178,12 +198,9 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   constexpr int RPI = 8;                                    // rows of a transfer
   constexpr int kStageB = (BM + BN) * kRowB;
   constexpr int XI = BM / RPI / NW, WI = BN / RPI / NW;     // transfers a wave and stage
-  // scales: by way of registers in chunks of two stages, 16 bytes a row; else
-  // by transfers with their stage, 8 bytes a row
-  constexpr int SRowB = SCREG ? 16 : 8;
-  constexpr int SRows = 256 / SRowB;                        // rows of a scale transfer
-  constexpr int SI = ((BM + BN) * SRowB / 256 + NW - 1) / NW;
-  constexpr int kScaleB = SI * NW * 256;                    // scale bytes of a slot
+  using S = Scales<BM, BN, NW, NST, SCREG>;
+  constexpr bool GROUPS = !SCREG && S::kStages > 1;
+  constexpr int SRowB = S::kRowB, SI = S::kOps, kScaleB = S::kSlotB;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* lsc = lds + NST * kStageB;
   const int tid = threadIdx.x;
@@ -267,6 +284,11 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   auto swz = [](int row) { return row >> 1 & 7; };
   // of a wave's transfer i; the same for all of them but for a lone wave
   auto pc = [&](int i) { return (uint32_t)((lane & 7) ^ swz((w + NW * i) * RPI + pr)) * 16u; };
+  // the word of a row that a lane transfers: a row's are held at word ^ 2 * sswz
+  auto sswz = [](int row) { return row / S::kRows % S::kStages; };
+  static_assert(SCREG || (BM % S::kRows == 0 && NW % S::kStages == 0),
+                "an operation is all of x or all of W, a wave's are of one swizzle");
+  const uint32_t sword = (uint32_t)(lane % (SRowB / 4)) ^ (uint32_t)(w % S::kStages * 2);
   uint32_t xoff[XI], woff[WI], soff[SCREG ? 1 : SI];
   rsrc_t xs_r, ws_r;
   int ld_cols = BN;   // columns of the tile being fetched
@@ -289,10 +311,10 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
       ws_r = ws_of(t);
 #pragma unroll
       for (int i = 0; i < SI; ++i) {
-        const int row = (w + NW * i) * SRows + (lane >> 1);
+        const int row = (w + NW * i) * S::kRows + lane / (SRowB / 4);
         const int rr = row < BM ? row : row - BM;
         soff[i] = rr < (row < BM ? t.mrows : row < BM + BN ? t.ncols : 0)
-                      ? (uint32_t)rr * sld + (lane & 1) * 4 : kOOB;
+                      ? (uint32_t)rr * sld + sword * 4 : kOOB;
       }
     }
   };
@@ -308,14 +330,14 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
     for (int i = 0; i < WI; ++i)
       if (!HALVES || (w + NW * i) * RPI < ld_cols)
         dma16(w_r, sb + BM * kRowB + (w + NW * i) * 1024, woff[i] + ko[i & 1]);
-    if constexpr (!SCREG) {
-      const uint32_t b0 = (uint32_t)it * 8;
-      const uint32_t so = b0 + (lane & 1) * 4 < (uint32_t)sld ? b0 : kPastEnd;
+  };
+  auto issue_scales = [&](int it, int slot) {
+    const uint32_t b0 = (uint32_t)it * 8;
+    const uint32_t so = b0 + sword * 4 < (uint32_t)sld ? b0 : kPastEnd;
 #pragma unroll
-      for (int i = 0; i < SI; ++i)
-        dma4((w + NW * i) * SRows < BM ? xs_r : ws_r, lsc + slot * kScaleB + (w + NW * i) * 256,
-             soff[i] + so);
-    }
+    for (int i = 0; i < SI; ++i)
+      dma4((w + NW * i) * S::kRows < BM ? xs_r : ws_r, lsc + slot * kScaleB + (w + NW * i) * 256,
+           soff[i] + so);
   };
 
   // Scales by way of registers: a group is 64 bytes (K of 2048) of every row,
@@ -388,7 +410,14 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
         }
       }
     }
+    if constexpr (GROUPS) {
+      if (lit % S::kStages == 0) {
+        issue_scales(lit, chunks);
+        chunks = chunks + 1 == S::kSlots ? 0 : chunks + 1;
+      }
+    }
     issue(lit, lslot);
+    if constexpr (!SCREG && !GROUPS) issue_scales(lit, lslot);
     lslot = lslot + 1 == NST ? 0 : lslot + 1;
     ++lit;
   };
@@ -403,12 +432,13 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   const uint32_t xsc = (uint32_t)(wm * TM * 32 + m) * SRowB + 4 * h;
   const uint32_t wsc = (uint32_t)(BM + wn * TN * 32 + m) * SRowB + 4 * h;
 
-  int slot = 0, cslot = 1;
+  int slot = 0, cslot = S::kSlots - 1;
   f32x16 acc[TN][TM];
   u32x4 xo[2][TM], wo[2][TN];   // operands of two steps
   uint32_t sx[TM], sv[TN];      // scale words of a stage
   auto read_scales = [&](int it) {
-    const char* ss = SCREG ? lsc + cslot * kScaleB + it % 2 * 8 : lsc + slot * kScaleB;
+    const char* ss = lsc + (SCREG || GROUPS ? cslot : slot) * kScaleB +
+                     (it % S::kStages ^ (GROUPS ? sswz(m) : 0)) * 8;
 #pragma unroll
     for (int j = 0; j < TM; ++j) sx[j] = *(const uint32_t*)(ss + xsc + j * 32 * SRowB);
 #pragma unroll
@@ -448,14 +478,15 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
       // this stage is there once at most the transfers of the later ones
       // are outstanding; then the barrier makes every wave's part visible
       // and frees the buffer read in the previous iteration
-      constexpr int AH = NST - 2, OPS = XI + WI + SI;
+      // (a group's scales come on top and make the wait the longer one)
+      constexpr int AH = NST - 2, OPS = XI + WI + (SCREG || GROUPS ? 0 : SI);
       if (AH > 0 && has_ld)
         __builtin_amdgcn_s_waitcnt(vm_lds(AH * OPS));
       else
         __builtin_amdgcn_s_waitcnt(vm_lds(0));
       barrier_no_fence();
       fetch();
-      if (SCREG && it % 2 == 0) cslot ^= 1;
+      if ((SCREG || GROUPS) && it % S::kStages == 0) cslot = cslot + 1 == S::kSlots ? 0 : cslot + 1;
       if (!HALVES || wn * TN * 32 < cur.ncols) {
         read_scales(it);
         // a step's operand reads go before the products of the step before it
@@ -583,7 +614,8 @@ hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int dev, int cus) {
 //     124 (128 x 256: 134, 64 x 128: 142, 256^2: 154)
 //   64 x 64, four stages, where every tile has a unit to itself: 1 x 6144 x
 //     4096 8.8 (64 x 128, three stages: 13, 128^2: 20)
-//   64 x 128, three stages, where those have: 30 x 19878 x 9088 36 (64^2: 44)
+//   64 x 128, three stages, where those have: 8 x 18000 x 4096 13.5 (64^2:
+//     15.3)
 //   64 x 64, scales by way of registers, for more tiles than units: 91 rows
 //     of 14 experts x 7390 x 8576 108 (64 x 128: 113, 128^2: 118); 64 x 128
 //     where the rows fill it: 1024 x 4096 x 4096 17 (64^2: 21, 128^2: 20)
@@ -609,7 +641,7 @@ hipError_t launch_by_size(const MxArgs& a, hipStream_t stream) {
     return launch_tile<D, 256, 256, 4, 2, 2, true>(a, stream, dev, cus);
   if (avg >= 48 && tiles(128, 128) * 4 >= cus * 5)
     return launch_tile<D, 128, 128, 2, 2, 2, true>(a, stream, dev, cus);
-  if (a.K > 512 && tiles(64, 64) * 8 <= cus * 9)
+  if (a.K > 512 && tiles(64, 64) <= cus)
     return launch_tile<D, 64, 64, 2, 2, 4, false>(a, stream, dev, cus);
   if (tiles(64, 128) <= cus) return launch_tile<D, 64, 128, 2, 2, 3, false>(a, stream, dev, cus);
   if (avg > 64) return launch_tile<D, 64, 128, 2, 2, 2, true>(a, stream, dev, cus);

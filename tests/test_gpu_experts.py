@@ -431,6 +431,31 @@ def test_linear_half_tiles(rows, N):
     check_product(L.mxfp4_linear(x, w, dtype=torch().float32), values(x), values(w), 544)
 
 
+@pytest.mark.parametrize("rows,N,K", [(40, 17000, 1312), (70, 12200, 2080), (9, 20000, 1184),
+                                      (130, 10900, 800)])
+def test_linear_scale_groups(rows, N, K):
+    """64 x 128 tiles, whose scales come for four stages of 256 at a time: six,
+    nine, five and four stages, the last one short."""
+    x, w = held(rows, K, rows), held(N, K, N)
+    check_product(L.mxfp4_linear(x, w, dtype=torch().float32), values(x), values(w), K)
+
+
+@pytest.mark.parametrize("K", [544, 1184, 1312, 2336])
+def test_expert_linear_scale_groups_across_tiles(K):
+    """65 rows of each expert: more tiles than workgroups, so the ring of scale
+    groups runs on from one tile into the next."""
+    t = torch()
+    rows, E, N = 520, 8, 2400
+    x = held(rows, K, 3)
+    W = L.MXFP4(*(v.view(E, N, -1) for v in held(E * N, K, E)))
+    off = [65 * e for e in range(E + 1)]
+    y = L.mxfp4_expert_linear(x, W, t.tensor(off, dtype=t.int32, device=DEV), dtype=t.float32)
+    xv = values(x)
+    for e in range(E):
+        check_product(y[off[e]:off[e + 1]], xv[off[e]:off[e + 1]],
+                      values(L.MXFP4(W.codes[e], W.scales[e])), K, f"expert {e}")
+
+
 def test_expert_linear_half_tiles():
     t = torch()
     rows, E, N, K = 3900, 4, 4700, 544   # 19 tiles of columns and 17 or so of rows
