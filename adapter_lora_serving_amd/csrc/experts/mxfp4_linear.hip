@@ -149,11 +149,11 @@ __device__ __forceinline__ void find_tile(const MxArgs& a, int item, int& row, i
 
 // The scales in LDS: a ring of groups, each the next kRowB bytes of every
 // row's. By way of registers a group serves two stages. By transfers it is a
-// stage's own 8 bytes of a row, or in 64 x 128 tiles those of 4 stages, with
-// the first of them, which asks for a line a quarter as often: 256 x 6144 x
-// 4096 12.7 us against 15.4, 16 x 28672 x 4096 16.1 against 18.9. In 64 x 64
-// tiles, which have fewer rows to a wave, 128 x 4096 x 4096 takes 9.1 us that
-// way against 8.8.
+// stage's own 8 bytes of a row, or in the tiles of 128 columns those of 4
+// stages, with the first of them, which asks for a line a quarter as often:
+// 256 x 6144 x 4096 12.7 us against 15.4, 16 x 28672 x 4096 in 64 x 128 tiles
+// 16.1 against 18.9. In 64 x 64 tiles, which have fewer rows to a wave, 128 x
+// 4096 x 4096 takes 9.1 us that way against 8.8.
 template <int BM, int BN, int NW, int NST, bool SCREG>
 struct Scales {
   static constexpr int kRowB = SCREG ? 16 : NST > 2 && BM < BN ? 32 : 8;
@@ -615,7 +615,7 @@ hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int dev, int cus) {
 //   64 x 64, four stages, where every tile has a unit to itself: 1 x 6144 x
 //     4096 8.8 (64 x 128, three stages: 13, 128^2: 20)
 //   64 x 128, three stages, where those have: 8 x 18000 x 4096 13.5 (64^2:
-//     15.3)
+//     15.3); of them 32 x 128, four stages, where no more rows are there: 12.3
 //   64 x 64, scales by way of registers, for more tiles than units: 91 rows
 //     of 14 experts x 7390 x 8576 108 (64 x 128: 113, 128^2: 118); 64 x 128
 //     where the rows fill it: 1024 x 4096 x 4096 17 (64^2: 21, 128^2: 20)
@@ -643,7 +643,11 @@ hipError_t launch_by_size(const MxArgs& a, hipStream_t stream) {
     return launch_tile<D, 128, 128, 2, 2, 2, true>(a, stream, dev, cus);
   if (a.K > 512 && tiles(64, 64) <= cus)
     return launch_tile<D, 64, 64, 2, 2, 4, false>(a, stream, dev, cus);
-  if (tiles(64, 128) <= cus) return launch_tile<D, 64, 128, 2, 2, 3, false>(a, stream, dev, cus);
+  if (tiles(64, 128) <= cus) {
+    if (a.K > 512 && a.rows <= 32)
+      return launch_tile<D, 32, 128, 1, 4, 4, false>(a, stream, dev, cus);
+    return launch_tile<D, 64, 128, 2, 2, 3, false>(a, stream, dev, cus);
+  }
   if (avg > 64) return launch_tile<D, 64, 128, 2, 2, 2, true>(a, stream, dev, cus);
   return launch_tile<D, 64, 64, 2, 2, 2, true>(a, stream, dev, cus);
 }

@@ -440,6 +440,25 @@ def test_linear_scale_groups(rows, N, K):
     check_product(L.mxfp4_linear(x, w, dtype=torch().float32), values(x), values(w), K)
 
 
+@pytest.mark.parametrize("rows,N,K", [(32, 17000, 1312), (1, 20011, 544), (17, 16500, 2080)])
+@pytest.mark.parametrize("E", [1, 3])
+def test_linear_32_rows(rows, N, K, E):
+    t = torch()
+    x = held(rows, K, rows)
+    if E == 1:
+        w = held(N, K, N)
+        check_product(L.mxfp4_linear(x, w), values(x), values(w), K)
+        return
+    N //= 3
+    W = L.MXFP4(*(v.view(E, N, -1) for v in held(E * N, K, E)))
+    off = [0, rows // 2, rows // 2, rows]
+    y = L.mxfp4_expert_linear(x, W, t.tensor(off, dtype=t.int32, device=DEV))
+    xv = values(x)
+    for e in range(E):
+        check_product(y[off[e]:off[e + 1]], xv[off[e]:off[e + 1]],
+                      values(L.MXFP4(W.codes[e], W.scales[e])), K, f"expert {e}")
+
+
 @pytest.mark.parametrize("K", [544, 1184, 1312, 2336])
 def test_expert_linear_scale_groups_across_tiles(K):
     """65 rows of each expert: more tiles than workgroups, so the ring of scale
