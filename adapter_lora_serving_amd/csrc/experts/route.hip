@@ -18,7 +18,7 @@
 // expression per expert.
 //
 // What bounds it: issued instructions, not bytes. 8192 tokens x 256 experts,
-// top-8 of 4 of 8 groups, fp32: 8.1 us for 8.9 MB (1.9 us at the copy rate),
+// top-8 of 4 of 8 groups, fp32: 7.7 us for 8.9 MB (1.9 us at the copy rate),
 // of which 0.25 us a round of the top-k, 1.1 the groups. 16 lanes hold a token
 // of up to 256 experts, so that the reductions stay in a row of lanes (DPP; by way
 // of LDS shuffles with a wave's 64 lanes a row the same took 19 us) and a
