@@ -237,10 +237,11 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
 template <typename D>
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ rows, int64_t nrows,
                                                  int H, const int32_t* __restrict__ positions,
-                                                 const float* __restrict__ weights, int k,
+                                                 const float* __restrict__ weights, int T, int k,
                                                  const char* __restrict__ residual,
                                                  char* __restrict__ y) {
-  const int t = blockIdx.x;
+  const uint32_t t = block_of_grid();
+  if (t >= (uint32_t)T) return;
   const int64_t rowb = (int64_t)H * D::kBytes;
   for (int c = threadIdx.x * 16; c < rowb; c += 256 * 16) {
     float acc[D::kVec];
@@ -280,8 +281,8 @@ hipError_t launch_combine_experts(int dtype, const void* rows, int64_t nrows, in
                                   const void* residual, void* y, hipStream_t stream) {
   if (T == 0) return hipSuccess;
 #define GO(D)                                                                                 \
-  hipLaunchKernelGGL(k_combine<D>, dim3((unsigned)T), dim3(256), 0, stream, (const char*)rows, \
-                     nrows, H, positions, weights, k, (const char*)residual, (char*)y)
+  hipLaunchKernelGGL(k_combine<D>, grid_of(T), dim3(256), 0, stream, (const char*)rows, nrows, \
+                     H, positions, weights, T, k, (const char*)residual, (char*)y)
   if (dtype == 1) GO(BF16); else GO(F32);
 #undef GO
   return hipGetLastError();

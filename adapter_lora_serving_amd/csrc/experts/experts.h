@@ -8,6 +8,19 @@
 
 namespace lora {
 
+// A grid of `blocks` workgroups of 256 threads, and a workgroup's number in
+// it. A launch takes fewer than 2^32 threads along one dimension: of more it
+// runs the remainder modulo 2^32 and reports no error. So past 2^23 workgroups
+// the grid has a second dimension, whose last row may be past `blocks`.
+constexpr int64_t kGridX = (int64_t)1 << 23;
+inline dim3 grid_of(int64_t blocks) {
+  return dim3((unsigned)(blocks < kGridX ? blocks : kGridX),
+              (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ uint32_t block_of_grid() {
+  return blockIdx.y * (uint32_t)kGridX + blockIdx.x;
+}
+
 // Scores, groups and weights of lora_route_experts (see the C ABI).
 struct RouteArgs {
   int T, E, k;
