@@ -159,14 +159,14 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
   __shared__ int chosen[256 / L][kMaxTopK];
   const int l = threadIdx.x % L;
   const int tok = threadIdx.x / L;
-  const int t = blockIdx.x * (256 / L) + tok;
-  const bool live = t < a.T;
+  const uint32_t t = block_of_grid() * (256 / L) + tok;
+  const bool live = t < (uint32_t)a.T;
   const int e0 = l * V;
   auto fmax2 = [](float p, float q) { return fmaxf(p, q); };
   auto umax2 = [](uint32_t p, uint32_t q) { return max(p, q); };
 
   float x[V];
-  load_row<T, V>(logits + (int64_t)(live ? t : a.T - 1) * a.E, e0, a.E, x);
+  load_row<T, V>(logits + (int64_t)(live ? t : (uint32_t)a.T - 1) * a.E, e0, a.E, x);
 #pragma unroll
   for (int i = 0; i < V; ++i) x[i] = x[i] != x[i] ? -kInf : fminf(x[i], __FLT_MAX__);
 
@@ -356,8 +356,9 @@ hipError_t launch_route_experts(int dtype, const void* logits, const float* bias
   const int gs = a.E / a.groups;
   const uint32_t gmagic = (1u << 21) / (uint32_t)gs + 1u;
 #define LAUNCH(TT, LV, VV)                                                                     \
-  hipLaunchKernelGGL((k_route<TT, LV, VV>), dim3((unsigned)((a.T + 256 / LV - 1) / (256 / LV))), \
-                     dim3(256), 0, stream, (const TT*)logits, bias, a, gs, gmagic, ids, weights)
+  hipLaunchKernelGGL((k_route<TT, LV, VV>),                                                    \
+                     grid_of(((int64_t)a.T + 256 / LV - 1) / (256 / LV)), dim3(256), 0, stream, \
+                     (const TT*)logits, bias, a, gs, gmagic, ids, weights)
 #define BY_E(TT)                              \
   do {                                        \
     if (a.E <= 16) LAUNCH(TT, 16, 1);         \

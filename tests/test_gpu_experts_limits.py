@@ -21,3 +21,19 @@ def test_combine_of_many_tokens(T):
     L.combine_experts(rows, pos, t.full((T, 1), 2.0, device=DEV), y=y)
     want = 2 * (pos + 1).bfloat16().expand(T, 8)
     assert t.equal(y, want)
+
+
+@pytest.mark.parametrize("T,E,live", [((1 << 28) + 5, 2, 1), ((1 << 28) - 1, 2, 1),
+                                      ((1 << 26) + 3, 257, 256)])
+def test_route_of_many_tokens(T, E, live):
+    """16 lanes a token (64 past 256 experts): from 2^28 (2^26) tokens on that
+    is 2^32 threads and more."""
+    t = torch()
+    x = t.zeros(T, E, dtype=t.bfloat16, device=DEV)
+    x[:, live] = 1.0
+    x[1::2, 0] = 2.0
+    out = L.Routing(t.full((T, 1), -5, dtype=t.int32, device=DEV), t.zeros(T, 1, device=DEV))
+    L.route_experts(x, 1, out=out)
+    del x
+    assert bool((out.ids[0::2] == live).all()) and bool((out.ids[1::2] == 0).all())
+    assert bool((out.weights == 1).all())
