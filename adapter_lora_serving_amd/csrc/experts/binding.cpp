@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/clamp.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Exceptions.h>
@@ -59,9 +60,15 @@ struct Call {
     if (o == Py_None) return std::nullopt;
     return tensor(o, name);
   }
+  // Indices as int32. What a wider type holds past int32 becomes int32's end
+  // and so stays out of range: cut to 32 bits, 2^32 + 3 would be index 3.
   at::Tensor int32(PyObject* o, const char* name) {
     at::Tensor t = tensor(o, name);
-    return t.scalar_type() == at::kInt ? t : t.to(at::kInt);
+    const at::ScalarType st = t.scalar_type();
+    if (st == at::kInt) return t;
+    if (st == at::kUInt32 || st == at::kUInt64) t = t.to(at::kLong);
+    if (t.scalar_type() == at::kLong) t = at::clamp(t, INT32_MIN, INT32_MAX);
+    return t.to(at::kInt);
   }
   at::Tensor make(at::IntArrayRef shape, at::ScalarType dtype) const {
     return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, (c10::DeviceIndex)dev));

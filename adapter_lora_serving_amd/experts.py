@@ -5,10 +5,11 @@ back to tokens.
 As in the package's other functions, arguments are marshalled to the C ABI of
 include/lora_mi355x.h on torch's current stream and the computation runs in
 the HIP kernels; invalid arguments raise LoraError before anything is
-enqueued. Outputs are allocated from torch unless they are passed in. The
-marshalling is compiled (csrc/experts/binding.cpp, built as _experts.so next
-to this file): a decode step's operators take less time than such calls in
-Python.
+enqueued. Outputs are allocated from torch unless they are passed in. Index
+tensors are int32; other types are converted first, and an int64 value that
+int32 does not hold stays out of range. The marshalling is compiled
+(csrc/experts/binding.cpp, built as _experts.so next to this file): a decode
+step's operators take less time than such calls in Python.
 """
 from __future__ import annotations
 

@@ -1,0 +1,59 @@
+"""The Python binding of the routed-expert operators on the GPU: types of index
+tensors, unusual arguments, and calls from several threads and streams."""
+import numpy as np
+import pytest
+
+import adapter_lora_serving_amd as L
+from gpu_util import f64, torch
+from oracle import experts_oracle as X
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+FAR = [2**32 + 3, -2**32 + 3, 2**33, 2**63 - 1, -2**63, -2**31 - 1, 2**31]
+
+
+def far_ids(T, k, E):
+    """int64 choices, some far outside int32 whose low half is an expert."""
+    rng = np.random.default_rng(T)
+    ids = rng.integers(0, E, (T, k))
+    at = rng.random((T, k)) < 0.4
+    ids[at] = rng.choice(FAR, at.sum())
+    return ids
+
+
+@pytest.mark.parametrize("T,k,E", [(7, 2, 8), (300, 4, 100), (17000, 4, 16)])
+def test_rows_of_wide_indices(T, k, E):
+    t = torch()
+    ids = far_ids(T, k, E)
+    slot = np.random.default_rng(1).integers(-1, 9, T)
+    r = L.expert_rows(t.from_numpy(ids).to(DEV), E, t.from_numpy(slot).to(DEV))
+    for got, want, name in zip(r, X.expert_rows(ids, E, slot), r._fields):
+        assert np.array_equal(got.cpu().numpy(), want), name
+
+
+@pytest.mark.parametrize("name", ["uint8", "int8", "int16", "uint32", "int64"])
+def test_index_types(name):
+    t = torch()
+    ids = t.randint(0, 8, (50, 2), device=DEV)
+    want = L.expert_rows(ids.int(), 8, ids[:, 0].contiguous().int())
+    typed = ids.to(getattr(t, name))
+    got = L.expert_rows(typed, 8, typed[:, 0].contiguous())
+    assert all(t.equal(a, b) for a, b in zip(got, want))
+
+
+def test_wide_indices_of_the_other_operators():
+    t = torch()
+    rows = t.randn(6, 64, device=DEV)
+    far = t.tensor(FAR, device=DEV)
+    # a position outside the rows adds nothing
+    y = L.combine_experts(rows, far.unsqueeze(1), t.ones(len(FAR), 1, device=DEV))
+    assert bool((y == 0).all())
+    # a row's token is clamped to the tokens
+    got, _ = L.gather_quantize_mxfp4(rows, far)
+    assert t.equal(got, rows[far.clamp(0, 5)])
+    # so are the experts' bounds: rows 0 and 1 are of expert 0, the others of expert 1
+    x = L.quantize_mxfp4(rows)
+    w = L.quantize_mxfp4(t.randn(2, 16, 64, device=DEV))
+    y = L.mxfp4_expert_linear(x, w, t.tensor([-2**32, 2, 2**32 + 3], device=DEV))
+    assert t.equal(y, L.mxfp4_expert_linear(x, w, t.tensor([0, 2, 6], device=DEV)))
+    assert not bool((f64(y)[5] == 0).all())
