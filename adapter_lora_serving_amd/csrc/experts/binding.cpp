@@ -193,12 +193,14 @@ PyObject* route(PyObject* const* a) {
   const c10::DeviceGuard guard(x.device());
   const at::Tensor ids = ids_in ? *ids_in : c.make({T, k}, at::kInt);
   const at::Tensor w = w_in ? *w_in : c.make({T, k}, at::kFloat);
+  const int renormalize = PyObject_IsTrue(a[7]);
+  if (renormalize < 0) throw python_error();
   const double scaling = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred()) throw python_error();
   check(lora_route_experts(dt, ptr(x), T, (int32_t)E, k, integer32(a[2], "scores"),
                            as<const float>(bias), integer32(a[4], "groups"),
                            integer32(a[5], "top_groups"), integer32(a[6], "group_score"),
-                           PyObject_IsTrue(a[7]) == 1, (float)scaling, as<int32_t>(ids),
+                           renormalize, (float)scaling, as<int32_t>(ids),
                            as<float>(w), c.stream()),
         "lora_route_experts");
   return pack({&ids, &w});

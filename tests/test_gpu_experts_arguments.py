@@ -57,3 +57,10 @@ def test_wide_indices_of_the_other_operators():
     y = L.mxfp4_expert_linear(x, w, t.tensor([-2**32, 2, 2**32 + 3], device=DEV))
     assert t.equal(y, L.mxfp4_expert_linear(x, w, t.tensor([0, 2, 6], device=DEV)))
     assert not bool((f64(y)[5] == 0).all())
+
+
+def test_route_flag_without_a_truth_value():
+    x = torch().zeros(2, 8, device=DEV)
+    with pytest.raises(ValueError):   # numpy's own error, as it was raised
+        L.route_experts(x, 2, renormalize=np.array([True, False]))
+    assert L.route_experts(x, 2, renormalize=np.bool_(True)).weights.tolist() == [[0.5, 0.5]] * 2
