@@ -31,7 +31,7 @@ lora_status check_choices(int64_t T, int32_t top_k, int32_t num_experts) {
   if (T < 0) return LORA_ERR_INVALID_ARG;
   if (top_k < 1 || top_k > lora::kMaxTopK || num_experts < 1 || num_experts > lora::kMaxExperts)
     return LORA_ERR_UNSUPPORTED;
-  if (T * top_k > kMaxI32) return LORA_ERR_INVALID_ARG;
+  if (T > kMaxI32 / top_k) return LORA_ERR_INVALID_ARG;   // T * top_k may pass 64 bits
   return LORA_OK;
 }
 

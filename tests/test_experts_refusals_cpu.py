@@ -1,0 +1,29 @@
+"""More refusals of the routed-expert operators, on the CPU: no call here
+reaches a kernel launch."""
+import os
+
+import pytest
+
+import adapter_lora_serving_amd as L
+from adapter_lora_serving_amd import build
+
+OK, INVALID, UNSUPPORTED, ALIGN, WORKSPACE = 0, 1, 2, 3, 4
+A16 = 0x10000   # a device address that is never dereferenced here
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not (os.path.exists(L.lib_path()) and os.path.exists(build.BINDING_PATH)):
+        build.build()
+    return L.lib()
+
+
+@pytest.mark.parametrize("T,k", [(1 << 59, 32), ((1 << 59) + 1, 32), (1 << 62, 4), ((1 << 63) - 1, 2),
+                                 (1 << 31, 1), (1 << 30, 2)])
+def test_choices_past_64_bits_are_refused(lib, T, k):
+    """T * k is a multiple of 2^64 in the first rows, so its low bits look small."""
+    assert lib.lora_route_experts(1, A16, T, 64, k, 0, None, 1, 1, 0, 1, 1.0, A16, A16,
+                                  None) == INVALID
+    assert lib.lora_expert_rows(A16, T, k, 8, None, A16, A16, A16, None, None, 0, None) == INVALID
+    assert lib.lora_expert_rows_workspace_bytes(T, k, 8) == 0
+    assert lib.lora_combine_experts(1, A16, 8, 64, A16, A16, T, k, None, A16, None) == INVALID
