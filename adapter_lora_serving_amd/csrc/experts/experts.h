@@ -37,7 +37,9 @@ hipError_t launch_route_experts(int dtype, const void* logits, const float* bias
                                 const RouteArgs& a, int32_t* ids, float* weights,
                                 hipStream_t stream);
 
-// Expert-sorted rows of T * k choices (lora_expert_rows).
+// Expert-sorted rows of T * k choices (lora_expert_rows): at most so many that
+// a count rounded up to a block of 1024 is an int.
+constexpr int64_t kMaxSortedChoices = ((int64_t)1 << 31) - 1024;
 size_t expert_rows_workspace_bytes(int64_t T, int k, int E);
 hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int32_t* token_slot,
                               int32_t* row_token, int32_t* positions, int32_t* offsets,

@@ -35,6 +35,12 @@ lora_status check_choices(int64_t T, int32_t top_k, int32_t num_experts) {
   return LORA_OK;
 }
 
+// The sort counts in blocks of 1024 choices, in 32 bits.
+lora_status check_sorted_choices(int64_t T, int32_t top_k, int32_t num_experts) {
+  const lora_status st = check_choices(T, top_k, num_experts);
+  return st == LORA_OK && T * top_k > lora::kMaxSortedChoices ? LORA_ERR_INVALID_ARG : st;
+}
+
 lora_status linear_impl(int dtype, const uint8_t* x_codes, const uint8_t* x_scales, int64_t rows,
                         const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
                         const int32_t* offsets, int32_t num_experts, void* y, void* stream) {
@@ -98,7 +104,7 @@ lora_status lora_route_experts(int dtype, const void* logits, int64_t T, int32_t
 }
 
 size_t lora_expert_rows_workspace_bytes(int64_t T, int32_t top_k, int32_t num_experts) {
-  if (check_choices(T, top_k, num_experts) != LORA_OK) return 0;
+  if (check_sorted_choices(T, top_k, num_experts) != LORA_OK) return 0;
   return lora::expert_rows_workspace_bytes(T, top_k, num_experts);
 }
 
@@ -106,7 +112,7 @@ lora_status lora_expert_rows(const int32_t* ids, int64_t T, int32_t top_k, int32
                              const int32_t* token_slot, int32_t* row_token, int32_t* positions,
                              int32_t* offsets, int32_t* row_slot, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  const lora_status st = check_choices(T, top_k, num_experts);
+  const lora_status st = check_sorted_choices(T, top_k, num_experts);
   if (st != LORA_OK) return st;
   if (!offsets) return LORA_ERR_INVALID_ARG;
   if (T > 0 && (!ids || !row_token || !positions)) return LORA_ERR_INVALID_ARG;

@@ -494,8 +494,9 @@ lora_status lora_route_experts(int dtype, const void* logits, int64_t T, int32_t
  *   row_slot  [T * top_k]     token_slot of each row's token, -1 for a dead
  *                             row (NULL exactly where token_slot is NULL)
  * offsets and row_slot are what lora_build_addressing_experts and
- * lora_apply_linear_from_experts take. The workspace (contents need no
- * initialisation) holds lora_expert_rows_workspace_bytes.
+ * lora_apply_linear_from_experts take. T * top_k is at most 2^31 - 1024 here.
+ * The workspace (contents need no initialisation) holds
+ * lora_expert_rows_workspace_bytes.
  */
 lora_status lora_expert_rows(const int32_t* ids, int64_t T, int32_t top_k, int32_t num_experts,
                              const int32_t* token_slot, int32_t* row_token, int32_t* positions,

@@ -27,3 +27,15 @@ def test_choices_past_64_bits_are_refused(lib, T, k):
     assert lib.lora_expert_rows(A16, T, k, 8, None, A16, A16, A16, None, None, 0, None) == INVALID
     assert lib.lora_expert_rows_workspace_bytes(T, k, 8) == 0
     assert lib.lora_combine_experts(1, A16, 8, 64, A16, A16, T, k, None, A16, None) == INVALID
+
+
+@pytest.mark.parametrize("n", [(1 << 31) - 1, (1 << 31) - 255, (1 << 31) - 1023])
+@pytest.mark.parametrize("E", [8, 1023, 1024])
+def test_rows_whose_blocks_pass_32_bits_are_refused(lib, n, E):
+    """Rounded up to whole blocks of 1024 choices, n is 2^31."""
+    need = lib.lora_expert_rows_workspace_bytes(n, 1, E)
+    assert need == 0
+    assert lib.lora_expert_rows(A16, n, 1, E, None, A16, A16, A16, None, A16, 1 << 40,
+                                None) == INVALID
+    need = lib.lora_expert_rows_workspace_bytes((1 << 31) - 1024, 1, E)
+    assert need == (0 if E == 1024 else ((1 << 21) - 1) * (E + 1) * 4)
