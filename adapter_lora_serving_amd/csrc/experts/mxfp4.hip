@@ -145,7 +145,7 @@ hipError_t launch_quantize_mxfp4(int dtype, int form, const void* x, int64_t src
   if (rows == 0) return hipSuccess;
   const int sld = mx_scale_row(K);
   const int64_t chunks = rows * sld * 4;   // of 8 values, over a row and its padding blocks
-  if (chunks > 0x7fffffff) return hipErrorInvalidValue;
+  if (chunks > (int64_t)1 << 31) return hipErrorInvalidValue;   // 2^27 rows of 32 are 2^31
   const unsigned blocks = (unsigned)((chunks + 255) / 256);
   const Divider per_row = divider((uint32_t)sld * 4);
 #define GO(D, F)                                                                               \

@@ -37,3 +37,21 @@ def test_route_of_many_tokens(T, E, live):
     del x
     assert bool((out.ids[0::2] == live).all()) and bool((out.ids[1::2] == 0).all())
     assert bool((out.weights == 1).all())
+
+
+@pytest.mark.parametrize("rows,K", [(1 << 27, 32), (1 << 20, 4096)])
+def test_quantize_of_2_to_the_32_values(rows, K):
+    """The largest quantisation: with 32 columns its rows and their padding are
+    2^31 pieces of 8."""
+    t = torch()
+    part = t.randn(1 << 10, K, device=DEV).bfloat16()
+    x = part.repeat(rows >> 10, 1)
+    x[-1] = 7.0
+    want, last = L.quantize_mxfp4(part), L.quantize_mxfp4(x[-1:].contiguous())
+    q = L.quantize_mxfp4(x)
+    assert t.equal(q.codes[-1:], last.codes) and t.equal(q.scales[-1:], last.scales)
+    q.codes[-1], q.scales[-1] = want.codes[-1], want.scales[-1]
+    for got, one in zip(q, want):
+        assert bool((got.view(-1, *one.shape) == one).all())
+    back = L.dequantize_mxfp4(q)
+    assert bool((back.view(-1, *part.shape) == L.dequantize_mxfp4(want)).all())
