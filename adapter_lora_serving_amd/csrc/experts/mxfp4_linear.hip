@@ -76,6 +76,12 @@ __device__ __forceinline__ void lds_barrier() {
   barrier_no_fence();
 }
 
+// Tiles of `tile` that hold n rows or columns; n up to 2^31 - 1, whose sum with
+// the tile is no int any more.
+__host__ __device__ __forceinline__ int tiles_of(int n, int tile) {
+  return (int)(((uint32_t)n + (uint32_t)tile - 1) / (uint32_t)tile);
+}
+
 // The current device and its compute units (asked for once per device).
 constexpr int kMaxDevices = 64;
 hipError_t compute_units(int* dev, int* n) {
@@ -97,7 +103,7 @@ template <typename D>
 __device__ __forceinline__ void zero_dead_rows(const MxArgs& a) {
   const int lo = min(max(a.offsets[0], 0), a.rows);
   const int hi = min(max(a.offsets[a.E], lo), a.rows);
-  const int64_t dead = (int64_t)(lo + a.rows - hi) * a.N;
+  const int64_t dead = ((int64_t)lo + (a.rows - hi)) * a.N;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < dead;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t at = i < (int64_t)lo * a.N ? i : i + (int64_t)(hi - lo) * a.N;
@@ -109,12 +115,12 @@ __device__ __forceinline__ void zero_dead_rows(const MxArgs& a) {
 // more than bounds in order can give, whatever the bounds are.
 template <int BM>
 __device__ __forceinline__ int count_tiles(const MxArgs& a) {
-  const int most = (a.rows + BM - 1) / BM + a.E;
+  const int most = tiles_of(a.rows, BM) + a.E;
   int tiles = 0;
   for (int s = lane_id(); s < a.E; s += kWave) {
     int beg, len;
     segment_of(a.offsets, s, a.rows, beg, len);
-    tiles = min(tiles + (len + BM - 1) / BM, most);
+    tiles = min(tiles + tiles_of(len, BM), most);
   }
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) tiles = min(tiles + __shfl_xor(tiles, d), most);
@@ -130,7 +136,7 @@ __device__ __forceinline__ void find_tile(const MxArgs& a, int item, int& row, i
   for (int s0 = 0; s0 < a.E; s0 += kWave) {
     int beg = 0, len = 0;
     if (s0 + lane < a.E) segment_of(a.offsets, s0 + lane, a.rows, beg, len);
-    const int tiles = (len + BM - 1) / BM;
+    const int tiles = tiles_of(len, BM);
     const int upto = before + wave_inclusive_scan(tiles);
     const uint64_t past = __ballot(upto > item);
     if (past != 0) {
@@ -211,7 +217,7 @@ k_mx_tile(MxArgs a, int sld, int ntiles) {
   const int kt = (a.K + kStageK - 1) / kStageK;   // at least NST - 1 (the walk looks one tile ahead)
 
   // the experts' row tiles; rows of no expert become zero
-  int mtiles = (a.rows + BM - 1) / BM;
+  int mtiles = tiles_of(a.rows, BM);
   if (a.offsets) {
     mtiles = count_tiles<BM>(a);
     zero_dead_rows<D>(a);
@@ -588,8 +594,8 @@ template <typename D, int BM, int BN, int WM, int WN, int NST, bool SCREG>
 hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int dev, int cus) {
   constexpr int NW = WM * WN;
   constexpr int lds = lds_bytes<BM, BN, NW, NST, SCREG>();
-  const int64_t mt = (a.rows + BM - 1) / BM + (a.offsets ? a.E : 0);
-  const int64_t nt = (a.N + BN - 1) / BN;
+  const int64_t mt = (int64_t)tiles_of(a.rows, BM) + (a.offsets ? a.E : 0);
+  const int64_t nt = tiles_of(a.N, BN);
   if (mt * nt > 0x7fffffff) return hipErrorInvalidValue;
   constexpr int occ = occupancy<BM, BN, NW, NST, SCREG>();
   const int64_t grid = std::min<int64_t>(8 * ((mt * nt + 7) / 8), (int64_t)cus * occ / 8 * 8);
@@ -627,8 +633,8 @@ hipError_t launch_by_size(const MxArgs& a, hipStream_t stream) {
   const int used = std::min(a.E, a.rows);   // experts with rows, at most
   const int avg = a.rows / used;
   auto tiles = [&](int bm, int bn) {
-    const int64_t mt = (a.rows + bm - 1) / bm + (a.offsets ? used / 2 : 0);
-    return std::max<int64_t>(mt, used) * ((a.N + bn - 1) / bn);
+    const int64_t mt = (int64_t)tiles_of(a.rows, bm) + (a.offsets ? used / 2 : 0);
+    return std::max<int64_t>(mt, used) * tiles_of(a.N, bn);
   };
   // a group of scale registers is 16 bytes of a row at the least, and a walk
   // through NST stages needs tiles of NST - 1

@@ -55,3 +55,27 @@ def test_quantize_of_2_to_the_32_values(rows, K):
         assert bool((got.view(-1, *one.shape) == one).all())
     back = L.dequantize_mxfp4(q)
     assert bool((back.view(-1, *part.shape) == L.dequantize_mxfp4(want)).all())
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_product_of_2_to_the_31_rows(grouped):
+    """One row less than 2^31, whose number and a tile's pass 31 bits."""
+    t = torch()
+    rows, N, K = (1 << 31) - 1, 2, 32
+    part = L.quantize_mxfp4(t.randn(1 << 15, K, device=DEV))
+    x = L.MXFP4(t.empty(rows, K // 2, dtype=t.uint8, device=DEV),
+                t.empty(rows, 4, dtype=t.uint8, device=DEV))
+    for to, one in zip(x, part):
+        whole = to[:rows >> 15 << 15].view(-1, *one.shape)
+        whole.copy_(one.expand_as(whole))
+        to[rows >> 15 << 15:].copy_(one[:rows & 0x7fff])
+    w = L.quantize_mxfp4(t.randn(2, N, K, device=DEV))
+    one = [L.mxfp4_linear(part, L.MXFP4(w.codes[e], w.scales[e])) for e in range(2)]
+    if grouped:   # a row of expert 0, the others of expert 1 but for the last
+        y = L.mxfp4_expert_linear(x, w, t.tensor([0, 1, rows - 1], device=DEV))
+        assert t.equal(y[0], one[0][0]) and bool((y[-1] == 0).all())
+        y[0], y[-1] = one[1][0], one[1][(rows - 1) & 0x7fff]
+    else:
+        y = L.mxfp4_linear(x, L.MXFP4(w.codes[1], w.scales[1]))
+    assert bool((y[:rows >> 15 << 15].view(-1, 1 << 15, N) == one[1]).all())
+    assert t.equal(y[rows >> 15 << 15:], one[1][:rows & 0x7fff])
