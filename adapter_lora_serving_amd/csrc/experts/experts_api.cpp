@@ -88,7 +88,7 @@ lora_status lora_route_experts(int dtype, const void* logits, int64_t T, int32_t
   if (top_k > num_experts / groups * top_groups) return LORA_ERR_INVALID_ARG;
   if (T == 0) return LORA_OK;
   if (!logits || !ids || !weights) return LORA_ERR_INVALID_ARG;
-  if (!aligned16(logits)) return LORA_ERR_ALIGNMENT;
+  if (!aligned16(logits) || !aligned4(bias)) return LORA_ERR_ALIGNMENT;
   lora::RouteArgs a;
   a.T = (int)T;
   a.E = num_experts;

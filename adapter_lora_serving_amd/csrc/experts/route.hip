@@ -116,8 +116,9 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// One of a lane's V consecutive values of a row of E, -inf past its end.
-template <typename T, int V>
+// One of a lane's V consecutive values of a row of E, -inf past its end. The
+// row's V values start on ALIGN bytes where they are read as whole vectors.
+template <typename T, int V, int ALIGN = sizeof(T) * V < 16 ? sizeof(T) * V : 16>
 __device__ __forceinline__ void load_row(const T* row, int e0, int E, float* x) {
   if (E % V == 0) {   // a row starts on V values: whole vectors
     if (e0 >= E) {
@@ -125,7 +126,7 @@ __device__ __forceinline__ void load_row(const T* row, int e0, int E, float* x) 
       for (int i = 0; i < V; ++i) x[i] = -kInf;
       return;
     }
-    struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack { T v[V]; };
+    struct alignas(ALIGN) Pack { T v[V]; };
     const Pack p = *(const Pack*)(row + e0);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -193,7 +194,7 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits,
   uint32_t key[V];
   float b[V];
   if (bias) {
-    load_row<float, V>(bias, e0, a.E, b);
+    load_row<float, V, 4>(bias, e0, a.E, b);   // a view of any element on
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] += s[i];
   } else {

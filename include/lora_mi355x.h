@@ -476,8 +476,8 @@ enum { LORA_QUANTIZE_PLAIN = 0, LORA_QUANTIZE_GATHER = 1, LORA_QUANTIZE_SILU_MUL
  * Equal values go to the lowest expert or group. An expert whose logit or c
  * is NaN or -inf is not available (a logit of +inf counts as the largest
  * finite float); where fewer than top_k are left, the remaining ids are -1
- * and their weights 0. groups is at most 16 and divides num_experts.
- * T = 1 and any T alike take one launch.
+ * and their weights 0. groups is at most 16 and divides num_experts. logits are
+ * 16-byte aligned, bias 4-byte aligned. T = 1 and any T alike take one launch.
  */
 lora_status lora_route_experts(int dtype, const void* logits, int64_t T, int32_t num_experts,
                                int32_t top_k, int32_t scores, const float* bias, int32_t groups,

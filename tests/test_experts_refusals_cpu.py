@@ -39,3 +39,9 @@ def test_rows_whose_blocks_pass_32_bits_are_refused(lib, n, E):
                                 None) == INVALID
     need = lib.lora_expert_rows_workspace_bytes((1 << 31) - 1024, 1, E)
     assert need == (0 if E == 1024 else ((1 << 21) - 1) * (E + 1) * 4)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_route_bias_between_floats_is_refused(lib, off):
+    assert lib.lora_route_experts(1, A16, 4, 64, 2, 0, A16 + off, 1, 1, 0, 1, 1.0, A16, A16,
+                                  None) == ALIGN

@@ -64,3 +64,19 @@ def test_route_flag_without_a_truth_value():
     with pytest.raises(ValueError):   # numpy's own error, as it was raised
         L.route_experts(x, 2, renormalize=np.array([True, False]))
     assert L.route_experts(x, 2, renormalize=np.bool_(True)).weights.tolist() == [[0.5, 0.5]] * 2
+
+
+@pytest.mark.parametrize("E", [16, 32, 64, 128, 256, 512, 1024, 60, 300])
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_route_bias_from_any_element(E, shift):
+    """A bias inside a larger tensor starts on any float."""
+    t = torch()
+    rng = np.random.default_rng(E + shift)
+    x = t.from_numpy((rng.integers(-32, 33, (9, E)) / 8).astype(np.float32)).to(DEV)
+    bias = t.from_numpy((rng.integers(-3, 4, E) / 16).astype(np.float32)).to(DEV)
+    packed = t.full((E + 8,), 100.0, device=DEV)
+    view = packed[shift:shift + E]
+    view.copy_(bias)
+    assert view.data_ptr() % 16
+    for got, want in zip(L.route_experts(x, 4, bias=view), L.route_experts(x, 4, bias=bias)):
+        assert t.equal(got, want)
