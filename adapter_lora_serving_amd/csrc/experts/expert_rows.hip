@@ -231,15 +231,15 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
 
 // y[t] = residual[t] + sum over j of weights[t, j] * rows[positions[t, j]],
 // j ascending in fp32, rounded once. A position outside [0, nrows) adds
-// nothing. 16 bytes of columns per thread, a workgroup a token: the rows'
-// bytes are the time. 8192 tokens x 8 rows x 4096 bf16 onto the residual: 132
-// us for 671 MB, 5.1 TB/s.
+// nothing. residual may be y (a thread reads its columns before it writes
+// them), so neither is __restrict__. 16 bytes of columns per thread, a
+// workgroup a token: the rows' bytes are the time. 8192 tokens x 8 rows x 4096
+// bf16 onto the residual: 132 us for 671 MB, 5.1 TB/s.
 template <typename D>
 __global__ __launch_bounds__(256) void k_combine(const char* __restrict__ rows, int64_t nrows,
                                                  int H, const int32_t* __restrict__ positions,
                                                  const float* __restrict__ weights, int T, int k,
-                                                 const char* __restrict__ residual,
-                                                 char* __restrict__ y) {
+                                                 const char* residual, char* y) {
   const uint32_t t = block_of_grid();
   if (t >= (uint32_t)T) return;
   const int64_t rowb = (int64_t)H * D::kBytes;

@@ -508,8 +508,8 @@ size_t lora_expert_rows_workspace_bytes(int64_t T, int32_t top_k, int32_t num_ex
  * lora_combine_experts: y[t] = residual[t] + sum over j of weights[t, j] *
  * rows[positions[t, j]], formed in float32 and rounded once to dtype. rows
  * [num_rows, width], residual (NULL: none) and y [T, width] are of dtype;
- * residual may be y. A position outside [0, num_rows) adds nothing, and its
- * weight is not read.
+ * residual may be y; y overlaps no other argument. A position outside
+ * [0, num_rows) adds nothing, and its weight is not read.
  */
 lora_status lora_combine_experts(int dtype, const void* rows, int64_t num_rows, int64_t width,
                                  const int32_t* positions, const float* weights, int64_t T,
