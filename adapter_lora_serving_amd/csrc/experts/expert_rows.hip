@@ -30,6 +30,13 @@ __device__ __forceinline__ void put_row(int i, int t, int row, bool live, int sl
   if (row_slot) row_slot[row] = live ? slot : -1;
 }
 
+// What a wave's lanes wrote to LDS before is what they read after it: LDS
+// operations of a wave are in order, so this holds the compiler alone.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // A decode step's few choices over few experts: one wave, no barrier (the
 // one-wave sort of the slot addressing, with the rows written in its place and
 // their slots asked for with the choices). 512 choices of 8 experts: 4.6 us;
@@ -52,22 +59,22 @@ __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ id
     slot[g] = row_slot && i < n ? token_slot[token_of(i, kmul)] : -1;
   }
   hist[lane] = 0;
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_order();
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const GroupMatch m = match_raw(raw[g], g * kWave + lane < n, E, nbits);
     key[g] = m.key < 0 ? 0 : m.key;   // lanes past n: any valid index, never used
     off[g] = hist[key[g]] + m.rank;
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     if (m.leader) hist[m.key] += m.count;   // distinct keys: no two leaders collide
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
   }
   const int c = lane <= E ? hist[lane] : 0;
   const int start = wave_inclusive_scan(c) - c;
   if (lane <= E) offsets[lane] = start;
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_order();
   hist[lane] = start;
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_order();
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int i = g * kWave + lane;
