@@ -45,3 +45,21 @@ def test_rows_whose_blocks_pass_32_bits_are_refused(lib, n, E):
 def test_route_bias_between_floats_is_refused(lib, off):
     assert lib.lora_route_experts(1, A16, 4, 64, 2, 0, A16 + off, 1, 1, 0, 1, 1.0, A16, A16,
                                   None) == ALIGN
+
+
+def test_compiled_binding_refuses_cpu_tensors(lib):
+    """Its own message: without the binding the same type says that it is not built."""
+    import torch
+    x = torch.zeros(2, 64)
+    i = torch.zeros(2, 2, dtype=torch.int32)
+    q = L.MXFP4(torch.zeros(2, 32, dtype=torch.uint8), torch.zeros(2, 4, dtype=torch.uint8))
+    for f in (lambda: L.route_experts(x, 2), lambda: L.expert_rows(i, 4),
+              lambda: L.combine_experts(x, i, torch.zeros(2, 2)), lambda: L.quantize_mxfp4(x),
+              lambda: L.gather_quantize_mxfp4(x, i[0]), lambda: L.silu_mul_quantize_mxfp4(x),
+              lambda: L.dequantize_mxfp4(q), lambda: L.mxfp4_linear(q, q),
+              lambda: L.mxfp4_expert_linear(q, q, i[0])):
+        with pytest.raises(L.LoraError, match="must be on the GPU"):
+            f()
+    for f in (lambda: L.route_experts([[0.0]], 1), lambda: L.dequantize_mxfp4([q[0], q[1]])):
+        with pytest.raises(L.LoraError, match="must be"):
+            f()
