@@ -80,3 +80,60 @@ def test_route_bias_from_any_element(E, shift):
     assert view.data_ptr() % 16
     for got, want in zip(L.route_experts(x, 4, bias=view), L.route_experts(x, 4, bias=bias)):
         assert t.equal(got, want)
+
+
+@pytest.mark.parametrize("E,G", [(512, 4), (1024, 4), (512, 16), (256, 2), (128, 8), (48, 3), (768, 12),
+                                 (96, 2), (1023, 11)])
+@pytest.mark.parametrize("group_score", ["max", "sum2"])
+def test_route_group_layouts(E, G, group_score):
+    """Groups of 1 to 16 whole lanes, and groups that cross lanes."""
+    t = torch()
+    rng = np.random.default_rng(E + G)
+    # distinct sums of distinct choices: no two groups are worth the same
+    x = np.stack([rng.permutation(E) for _ in range(12)]) / E + rng.random((12, 1))
+    x[rng.random(x.shape) < 0.3] = -np.inf
+    logits = t.from_numpy(x.astype(np.float32)).to(DEV)
+    r = L.route_experts(logits, 4, groups=G, top_groups=max(1, G // 2), group_score=group_score)
+    best = X.route(f64(logits), 4, groups=G, top_groups=max(1, G // 2), group_score=group_score)
+    assert np.array_equal(r.ids.cpu().numpy(), best[0])
+
+
+def test_calls_from_threads_on_their_own_streams():
+    """Two threads, a stream and a set of inputs each, at the same time."""
+    import threading
+    t = torch()
+
+    def inputs(seed):
+        g = t.Generator(device=DEV)
+        g.manual_seed(seed)
+        return (t.randn(300, 64, device=DEV, generator=g), t.randn(300, 512, device=DEV, generator=g),
+                t.randn(64, 256, 512, device=DEV, generator=g))
+
+    def layer(logits, x, w):
+        r = L.route_experts(logits, 4)
+        s = L.expert_rows(r.ids, 64)
+        rows, q = L.gather_quantize_mxfp4(x, s.row_token)
+        y = L.mxfp4_expert_linear(q, L.quantize_mxfp4(w), s.offsets, dtype=t.float32)
+        return L.combine_experts(y, s.positions, r.weights)
+
+    sets = [inputs(seed) for seed in (1, 2)]
+    want = [layer(*s) for s in sets]
+    t.cuda.synchronize()
+    got, failed = {}, []
+
+    def work(i):
+        try:
+            with t.cuda.stream(t.cuda.Stream()):
+                got[i] = [layer(*sets[i]) for _ in range(20)]
+                t.cuda.current_stream().synchronize()
+        except Exception as e:   # a failure of a thread has to reach the test
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed
+    for i in range(2):
+        assert len(got[i]) == 20 and all(t.equal(y, want[i]) for y in got[i])
