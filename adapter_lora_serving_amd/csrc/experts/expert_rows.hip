@@ -14,7 +14,7 @@
 namespace lora {
 
 // Token of choice i: i / k as a product with kmul = ceil(2^32 / k) (0 for k =
-// 1), exact where i k^2 < 2^32: for the 2^16 choices of one launch at most.
+// 1), exact where i k^2 < 2^32: for the 2^22 choices of one launch at most.
 __device__ __forceinline__ int token_of(int i, uint32_t kmul) {
   return kmul ? (int)__umulhi((uint32_t)i, kmul) : i;
 }
@@ -87,15 +87,22 @@ __global__ __launch_bounds__(64) void k_rows_wave(const int32_t* __restrict__ id
 // Larger batches in one launch: a workgroup places 1024 choices and counts
 // all n of them for itself, those before its own apart from the rest, so no
 // workgroup waits for another. The counting reads n ids from L2 a workgroup:
-// 65536 choices are 64 workgroups of 256 KB each; past that the two passes
-// of the addressing count once. 65536 choices of 256 experts: 10.4 us, bound by
-// the instructions and LDS adds of the counting (the two passes and the finish:
-// 17 us). Neighbouring lanes add to other copies of the counters, since lanes
+// 65536 choices are 64 workgroups of 256 KB each, 10.4 us for 256 experts,
+// bound by the instructions and LDS adds of the counting. Past that, where the
+// workspace of lora_expert_rows_workspace_bytes begins, the two passes of the
+// addressing count once, and a third launch writes the rows. One launch would
+// still be the shorter there (256 experts, 131072 choices: 15.7 us against
+// 42.2; 262144: 25 against 75; 1048576: 246 against 387). The two passes hold a
+// key a thread, 1023 experts and the dead choices; 1024 experts stay in one
+// launch while token_of is exact (131072 choices: 17.3 us against 309 in the
+// one workgroup that sorts any number of keys; 1048576: 348 against 2652).
+// Neighbouring lanes add to other copies of the counters, since lanes
 // that add to one address wait for each other: 4, 8 and 16 copies take 10.2,
 // 10.2 and 10.4 us where the choices are spread evenly, 18.8, 12.1 and 9.5
 // where all are of one expert (or dead). 16 fit the LDS up to 512 experts.
 constexpr int kRowsBlock = 1024;
 constexpr int kRowsOneLaunch = 1 << 16;
+constexpr int kRowsOneLaunchAllKeys = 1 << 22;
 
 template <int kCopies>
 __global__ __launch_bounds__(kRowsBlock) void k_rows_block(
@@ -214,7 +221,8 @@ hipError_t launch_expert_rows(const int32_t* ids, int T, int k, int E, const int
 #undef W
     return hipGetLastError();
   }
-  if (n <= kRowsOneLaunch) {
+  const bool two_passes = addressing_workspace_bytes(n, E) > 0;   // E + 1 keys, one a thread
+  if (n <= (two_passes ? kRowsOneLaunch : kRowsOneLaunchAllKeys)) {
     const int nb = n == 0 ? 1 : (n + kRowsBlock - 1) / kRowsBlock;
     const int copies = E <= 512 ? 16 : 8;
     auto* const f = copies == 16 ? k_rows_block<16> : k_rows_block<8>;

@@ -2,6 +2,7 @@
 
 Inputs repeat or are constant, so that what is expected needs no second pass
 over gigabytes on the host."""
+import numpy as np
 import pytest
 
 import adapter_lora_serving_amd as L
@@ -79,3 +80,25 @@ def test_product_of_2_to_the_31_rows(grouped):
         y = L.mxfp4_linear(x, L.MXFP4(w.codes[1], w.scales[1]))
     assert bool((y[:rows >> 15 << 15].view(-1, 1 << 15, N) == one[1]).all())
     assert t.equal(y[rows >> 15 << 15:], one[1][:rows & 0x7fff])
+
+
+@pytest.mark.parametrize("T,k,E", [(16384, 8, 1024), (16385, 8, 1024), (1 << 17, 32, 1024), (74899, 7, 1023),
+                                   (209715, 20, 1024), ((1 << 17) + 1, 32, 1024), (1 << 22, 1, 1024)])
+def test_rows_of_many_choices_and_experts(T, k, E):
+    """Around the largest sort of one launch, 2^22 choices of 1024 experts."""
+    t = torch()
+    rng = np.random.default_rng(T)
+    ids = rng.integers(-3, E + 3, (T, k)).astype(np.int32)
+    slot = rng.integers(-1, 50, T).astype(np.int32)
+    r = L.expert_rows(t.from_numpy(ids).to(DEV), E, t.from_numpy(slot).to(DEV))
+    key = ids.reshape(-1)
+    key = np.where((key < 0) | (key >= E), E, key)
+    order = np.argsort(key, kind="stable")
+    live = key[order] < E
+    positions = np.empty(T * k, np.int32)
+    positions[order] = np.arange(T * k)
+    counts = np.bincount(key, minlength=E + 1)[:E]
+    want = (order // k, np.where(key < E, positions, -1).reshape(T, k),
+            np.concatenate([[0], np.cumsum(counts)]), np.where(live, slot[order // k], -1))
+    for got, ref, name in zip(r, want, r._fields):
+        assert np.array_equal(got.cpu().numpy(), ref), name
