@@ -6,7 +6,9 @@ import numpy as np
 import pytest
 
 import adapter_lora_serving_amd as L
-from gpu_util import torch
+from gpu_util import f64, torch
+from oracle import experts_oracle as X
+from test_gpu_experts import check_product, check_quantized, held, values
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -102,3 +104,51 @@ def test_rows_of_many_choices_and_experts(T, k, E):
             np.concatenate([[0], np.cumsum(counts)]), np.where(live, slot[order // k], -1))
     for got, ref, name in zip(r, want, r._fields):
         assert np.array_equal(got.cpu().numpy(), ref), name
+
+
+@pytest.mark.parametrize("rows,N,K", [(3, 40, 1 << 20), (300, 130, (1 << 20) - 32), (40, 1 << 20, 96),
+                                      (1, (1 << 20) - 1, 544), (700, 1 << 20, 544)])
+def test_product_of_the_widest_operands(rows, N, K):
+    t = torch()
+    x, w = held(rows, K, 1), held(N, K, 2)
+    y = L.mxfp4_linear(x, w, dtype=t.float32)
+    check_product(y, values(x), values(w), K)
+
+
+@pytest.mark.parametrize("rows", [40, 5000])
+def test_product_of_the_most_experts(rows):
+    t = torch()
+    E, N, K = 1024, 72, 544
+    x, w = held(rows, K, 1), held(E * N, K, 2)
+    W = L.MXFP4(w.codes.view(E, N, -1), w.scales.view(E, N, -1))
+    off = np.sort(np.random.default_rng(rows).integers(0, rows + 1, E + 1)).astype(np.int32)
+    y = L.mxfp4_expert_linear(x, W, t.from_numpy(off).to(DEV), dtype=t.float32)
+    xv, wv = values(x), values(w).view(E, N, K)
+    dead = t.ones(rows, dtype=t.bool, device=DEV)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        dead[lo:hi] = False
+        if hi > lo:
+            check_product(y[lo:hi], xv[lo:hi], wv[e], K, f"expert {e}")
+    assert bool((y[dead] == 0).all())
+
+
+@pytest.mark.parametrize("K", [1 << 20, (1 << 20) - 32])
+def test_quantize_the_widest_rows(K):
+    t = torch()
+    x = t.randn(3, 2 * K, device=DEV).bfloat16()
+    act, q = L.silu_mul_quantize_mxfp4(x)
+    check_quantized(q, f64(act))
+    rows, g = L.gather_quantize_mxfp4(act, t.tensor([2, 0, 2, 1], device=DEV))
+    assert t.equal(rows, act[[2, 0, 2, 1]]) and t.equal(g.codes, q.codes[[2, 0, 2, 1]])
+    assert t.equal(L.dequantize_mxfp4(q), t.from_numpy(X.dequantize(*X.quantize(f64(act)))).to(DEV).bfloat16())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_combine_the_widest_rows(dtype):
+    t = torch()
+    rows = t.randint(-8, 9, (5, 1 << 20), device=DEV).to(t.bfloat16 if dtype == "bf16" else t.float32)
+    pos = t.tensor([[4, 0], [5, 3], [-1, 9]], device=DEV)
+    y = L.combine_experts(rows, pos, t.tensor([[2.0, 1.0], [1.0, -4.0], [1.0, 1.0]], device=DEV))
+    assert t.equal(y[0], 2 * rows[4] + rows[0]) and t.equal(y[1], -4 * rows[3])   # exact
+    assert bool((y[2] == 0).all())
