@@ -14,17 +14,19 @@
 // A and the x rows operand B, so a lane ends with runs of 4 columns of one
 // row of y.
 //
-// What bounds it (MI355X, 4.7 TB/s copy, 2.66 PFLOP/s largest fp8 product):
+// What bounds it (MI355X, 4.7 TB/s copy, 2.66 PFLOP/s largest fp8 product).
+// Cards differ: a range is that of several cards, its low end with the inputs
+// of the call before in the cache, its high end with other ones every time.
 //   few rows: the weight's bytes. 512 rows of 8 experts x 28672 x 4096: 113
-//     us, 4.7 TB/s of codes, scales and y.
-//   many rows: 8192 x 28672 x 4096 511 us, 3.8 PFLOP/s; 16384 rows of 8
-//     experts x 4096 x 14336 543 us, 3.5 (its 70 row tiles x 16 take 4.5 turns
-//     of the 256 units). Of the first one's time the products alone take 266
-//     us, waiting for their LDS operands 85, for the transfers 55, scales 20,
-//     and the way of y through LDS and out 70.
+//     to 129 us, 4.1 to 4.7 TB/s of codes, scales and y.
+//   many rows: 8192 x 28672 x 4096 493 to 558 us, 3.4 to 3.9 PFLOP/s; 16384
+//     rows of 8 experts x 4096 x 14336 538 to 564 us (its 70 row tiles x 16
+//     take 4.4 turns of the 256 units). Where the first one took 511 us, the
+//     products alone were 266 of them, waiting for their LDS operands 85, for
+//     the transfers 55, scales 20, and the way of y through LDS and out 70.
 //   few tiles (a decode step's dense projections): the walk over K, 0.3 us a
-//     stage of 256. 1 x 6144 x 4096: 8.6 us, of which the launch and the ends
-//     of the walk are 5.
+//     stage of 256. 1 x 6144 x 4096: 8.1 to 8.9 us, of which the launch and the
+//     ends of the walk are 5.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -177,7 +179,7 @@ struct Scales {
 // compute unit's 160 KB hold (at most 16 waves of them: with more, fewer
 // registers a wave than its accumulators and operands need). The compiler is
 // held to that many: with 20 registers more the 128 x 128 tile has one
-// workgroup a unit, and the 512-row product above takes 158 us.
+// workgroup a unit, and the 512-row product above took 158 us in place of 124.
 template <int BM, int BN, int NW, int NST, bool SCREG>
 constexpr int lds_bytes() {
   using S = Scales<BM, BN, NW, NST, SCREG>;
@@ -614,17 +616,21 @@ hipError_t launch_tile(const MxArgs& a, hipStream_t stream, int dev, int cus) {
 }
 
 // Tiles and depths by the sizes, mt x nt tiles of y for the compute units to
-// share. Every choice gives the same y. Measured (us, us of the others):
-//   256 x 256, where they fill the chip: 2048 x 6144 x 4096 38 (128^2: 45)
+// share. Every choice gives the same y. Measured on one card, other weights
+// every time (us, us of the others):
+//   256 x 256, where they fill the chip: 2048 x 6144 x 4096 38 (128^2: 44,
+//     64 x 128: 59)
 //   128 x 128, two workgroups a unit: 512 rows of 8 experts x 28672 x 4096
-//     124 (128 x 256: 134, 64 x 128: 142, 256^2: 154)
+//     129 (64 x 128: 140, 64^2: 148, 256^2: 158)
 //   64 x 64, four stages, where every tile has a unit to itself: 1 x 6144 x
-//     4096 8.8 (64 x 128, three stages: 13, 128^2: 20)
-//   64 x 128, three stages, where those have: 8 x 18000 x 4096 13.5 (64^2:
-//     15.3); of them 32 x 128, four stages, where no more rows are there: 12.3
+//     4096 8.8 (32 x 128: 10.3, 64 x 128, three stages: 11.7, 128^2: 21)
+//   64 x 128, three stages, where those have: 40 x 18000 x 4096 15.3 (64^2:
+//     19.5, 128^2: 22); of them 32 x 128, four stages, where no more rows are
+//     there: 8 x 18000 x 4096 13.1 (64 x 128: 14.8)
 //   64 x 64, scales by way of registers, for more tiles than units: 91 rows
-//     of 14 experts x 7390 x 8576 108 (64 x 128: 113, 128^2: 118); 64 x 128
-//     where the rows fill it: 1024 x 4096 x 4096 17 (64^2: 21, 128^2: 20)
+//     of 14 experts x 7390 x 8576 111 (64 x 128: 114, 128^2: 120); 64 x 128
+//     where the rows fill it: 600 x 5300 x 1056 9.4 (64^2: 10.0, 128^2: 10.3),
+//     1024 x 4096 x 4096 21 (64^2: 23, 128^2: 21)
 template <typename D>
 hipError_t launch_by_size(const MxArgs& a, hipStream_t stream) {
   int dev = 0, cus = 0;
