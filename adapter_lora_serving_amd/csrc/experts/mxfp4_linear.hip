@@ -17,10 +17,10 @@
 // What bounds it (MI355X, 4.7 TB/s copy, 2.66 PFLOP/s largest fp8 product).
 // Cards differ: a range is that of several cards, its low end with the inputs
 // of the call before in the cache, its high end with other ones every time.
-//   few rows: the weight's bytes. 512 rows of 8 experts x 28672 x 4096: 113
-//     to 129 us, 4.1 to 4.7 TB/s of codes, scales and y.
+//   few rows: the weight's bytes. 512 rows of 8 experts x 28672 x 4096: 108
+//     to 129 us, 4.1 to 4.9 TB/s of codes, scales and y.
 //   many rows: 8192 x 28672 x 4096 493 to 558 us, 3.4 to 3.9 PFLOP/s; 16384
-//     rows of 8 experts x 4096 x 14336 538 to 564 us (its 70 row tiles x 16
+//     rows of 8 experts x 4096 x 14336 533 to 564 us (its 70 row tiles x 16
 //     take 4.4 turns of the 256 units). Where the first one took 511 us, the
 //     products alone were 266 of them, waiting for their LDS operands 85, for
 //     the transfers 55, scales 20, and the way of y through LDS and out 70.
