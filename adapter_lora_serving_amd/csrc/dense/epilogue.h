@@ -208,7 +208,8 @@ constexpr int vm_lds_le(int n) { return vmcnt_le(n) & ~(15 << 8); }
 
 // h of a token, scaled, as `TERMS` bf16 parts whose sum it is: the high part
 // and what that leaves, so that the delta has h in 16 bits of fraction (2
-// terms, for a bf16 result) or all of its 24 (3 terms).
+// terms, for a bf16 result) or all of its 24 (3 terms). Values that do not fit
+// bf16 show in the high part and are not for the matrix unit.
 template <int TERMS>
 __device__ __forceinline__ void split_bf16(const float* v, u32x4* out) {
 #pragma unroll
@@ -221,9 +222,32 @@ __device__ __forceinline__ void split_bf16(const float* v, u32x4* out) {
       if (p + 1 == TERMS) break;
       x -= bf16lo(pair);
       y -= bf16hi(pair);
-      x = x == x ? x : 0.0f;   // nothing after an infinity
-      y = y == y ? y : 0.0f;
     }
+  }
+}
+
+// What the delta's values that do not fit bf16 (lora_common.h) come to for token t
+// at position p, added to v: columns [n, n + 8) of W's rows from `first` on.
+// Seldom called, so it is short code, not fast code.
+__device__ __forceinline__ void add_unfit(const LinearArgs& a, int64_t t, int p, int first, int n,
+                                          int64_t out, f32x4* v) {
+  const int s = slot_of_position(a.indptr, a.slots, p);
+  if (s >= a.slots) return;
+  int beg, len;
+  segment_of(a.indptr, s, a.T, beg, len);
+  if (p < beg || p >= beg + len) return;
+  const int r = clamp_rank(a.ranks[s], a.R);
+  const float scale = a.scalings[s];
+#pragma unroll 1
+  for (int q = 0; q < 8 && n + q < a.N; ++q) {
+    const int row = first + n + q;
+    int si = 0;
+    while (si + 1 < a.slices && a.off[si + 1] <= row) ++si;
+    const float* h = a.h + (t * a.slices + si) * a.R;
+    const uint16_t* b = (const uint16_t*)a.b + (s * out + row) * a.R;
+    const float z = unfit_sum(h, b, r, scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i / 4][i % 4] += i == q ? z : 0.0f;
   }
 }
 

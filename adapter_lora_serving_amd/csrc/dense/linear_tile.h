@@ -625,6 +625,7 @@ void k_linear_tile(LinearArgs a, int sld, int mtiles, int ntiles) {
     // and 16 ranks at a time: scaling * h as bf16 parts (other rows 0) against
     // the slot's B, on the accumulators. A turn is a few products and its loads
     // take 2 us, so the loads of kTurns turns are on their way at a time.
+    bool unfit = false;   // values that are not for the matrix unit: see add_unfit
     if (e.h) {
       // h in 24 bits of fraction where y is float32 or goes on to its codes, else in 16
       constexpr int TERMS = GATED && !OP::kWide ? 2 : 3;
@@ -759,6 +760,14 @@ void k_linear_tile(LinearArgs a, int sld, int mtiles, int ntiles) {
               for (int k = 0; k < 8; ++k)
                 if (k >= n) bb[d][i][k / 2] &= (k & 1) ? 0x0000ffffu : 0xffff0000u;
           }
+          uint32_t ends = 0;
+#pragma unroll
+          for (int i = 0; i < OT; ++i) ends |= not_finite(bb[d][i]);
+          if (__builtin_expect(__ballot(ends != 0) != 0, 0)) {
+            unfit = true;
+#pragma unroll
+            for (int i = 0; i < OT; ++i) bb[d][i] &= finite_halves(bb[d][i]);
+          }
 #pragma unroll
           for (int j = 0; j < TM; ++j)
             if (in_tile(now, j)) {
@@ -767,6 +776,12 @@ void k_linear_tile(LinearArgs a, int sld, int mtiles, int ntiles) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(hb[d][j][k / 4][k % 4]) * now.scale;
               split_bf16<TERMS>(v, hp);
+              if (__builtin_expect(__ballot(not_finite(hp[0]) != 0) != 0, 0)) {
+                unfit = true;
+                const u32x4 keep = finite_halves(hp[0]);
+#pragma unroll
+                for (int p = 0; p < TERMS; ++p) hp[p] &= keep;
+              }
 #pragma unroll
               for (int part = 0; part < PARTS; ++part)
                 if (now.part == part) {
@@ -815,6 +830,51 @@ void k_linear_tile(LinearArgs a, int sld, int mtiles, int ntiles) {
     };
     // rows and columns of this lane in tile (j, b), half k
     auto row_in = [&](int j, int k) { return wm * TM * 32 + j * 32 + k * 16 + lane / 4; };
+    // Seldom: tile by tile to LDS, what is unfit added there, and back. (In the loop
+    // below, where more is held, it costs the main loop registers; so do addresses
+    // that the compiler can form ahead of it, hence the lane that it cannot know.)
+    if (__builtin_expect(unfit, 0)) {
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      const int lm = ln & 31, lr = ln / 4;
+      auto chunk = [&](int row, int c) { return (f32x4*)(way + row * 128 + ((c ^ (row & 7)) << 4)); };
+#pragma unroll 1
+      for (int u = 0; u < TM * TN * 2; ++u) {
+        const int i = u / 2 % TN, j = u / 2 / TN, k = u % 2;
+#pragma unroll
+        for (int q = 0; q < TM * TN; ++q)
+          if (u / 2 == q && lm / 16 == k) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const f32x16& z = acc[q % TN][q / TN];
+              *chunk(lm % 16, 2 * c + ln / 32) = f32x4{z[4 * c], z[4 * c + 1], z[4 * c + 2], z[4 * c + 3]};
+            }
+          }
+        fence();
+        f32x4 v[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) v[c] = *chunk(lr, ln % 4 * 2 + c);
+        fence();
+        const int row = wm * TM * 32 + j * 32 + k * 16 + lr, p = cur.row + row;
+        if (row < cur.mrows)
+          add_unfit(e, token_of(p), p, GATED ? i / OT * e.N : 0, c0w + i % OT * 32 + ln % 4 * 8,
+                    GATED ? 2 * (int64_t)e.N : e.N, v);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) *chunk(lr, ln % 4 * 2 + c) = v[c];
+        fence();
+#pragma unroll
+        for (int q = 0; q < TM * TN; ++q)
+          if (u / 2 == q && lm / 16 == k) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const f32x4 z = *chunk(lm % 16, 2 * c + ln / 32);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[q % TN][q / TN][4 * c + x] = z[x];
+            }
+          }
+        fence();
+      }
+    }
     auto ahead_of = [&](int u) {
       Ahead<GATED> n;
       const int c = c0w + u % OT * 32 + lane % 4 * 8;

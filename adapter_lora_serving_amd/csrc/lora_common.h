@@ -137,6 +137,42 @@ __device__ __forceinline__ void segment_of(const int32_t* __restrict__ indptr, i
   n = e - b;
 }
 
+// The delta's values that bf16 parts cannot carry to the matrix unit: a scaled h
+// that is not finite or that bf16 rounds to infinity, and a B that is not finite. A
+// product with rows of several slots takes other slots' rows and other slices'
+// columns as zeros, and zero times these is no zero. They are taken as zeros
+// there, and what they come to is added to their own rows and columns in fp32.
+__device__ __forceinline__ bool fits_bf16(float v) {
+  return (__float_as_uint(v) & 0x7fffffffu) < 0x7f7f8000u;
+}
+// Not 0 where one of eight bf16 values is an infinity or a NaN: a unit more of an
+// exponent of all ones goes into the sign's place.
+__device__ __forceinline__ uint32_t not_finite(u32x4 v) {
+  uint32_t e = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) e |= (v[k] & 0x7f807f80u) + 0x00800080u;
+  return e & 0x80008000u;
+}
+// Mask of the finite ones.
+__device__ __forceinline__ u32x4 finite_halves(u32x4 v) {
+  u32x4 m;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    m[k] = ((v[k] & 0x7f80u) == 0x7f80u ? 0u : 0x0000ffffu) |
+           ((v[k] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+  return m;
+}
+// The sum of the products that one of them is a factor of, over r ranks.
+__device__ __forceinline__ float unfit_sum(const float* h, const uint16_t* b, int r, float scale) {
+  float z = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < r; ++k) {
+    const float x = h[k] * scale, y = __uint_as_float((uint32_t)b[k] << 16);
+    if (!fits_bf16(x) || !fits_bf16(y)) z = fmaf(x, y, z);
+  }
+  return z;
+}
+
 // Token index read from token_order, clamped into [0, T).
 __device__ __forceinline__ int token_at(const int32_t* __restrict__ order, int p, int T) {
   const int t = order[p];
