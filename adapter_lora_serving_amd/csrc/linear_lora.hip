@@ -30,7 +30,9 @@
 // slot's B rows of the tile's columns are staged in LDS, and the delta is
 // accumulated by two more MFMA K-steps (hi, lo) into the same accumulators
 // (h is thus effectively fp32). A tile lies in one out slice (every slice
-// width is a multiple of 256), so its h columns are that slice's.
+// width is a multiple of 256), so its h columns are that slice's. Infinities and
+// NaN in h or B, which would reach the other slots' rows through their zeros, are
+// staged as zeros and added to their own rows before the store.
 // The result is rounded once to bf16 (nearest even) and stored.
 #include "lora_common.h"
 #include "lora_kernels.h"
@@ -44,7 +46,8 @@ constexpr int kGK = 32;          // K per stage
 constexpr int kStages = 4;       // LDS ring: the stage being read + 3 in flight
 constexpr int kGThreads = 512;
 constexpr int kStageBytes = kGT * kGK * 2;   // one operand tile of one stage, bf16 (16 KB)
-// LDS: stage s holds [x tile][W tile] at s * 2 * kStageBytes; then token ids
+// LDS: stage s holds [x tile][W tile] at s * 2 * kStageBytes; then token ids, and
+// whether the delta has values that do not fit bf16
 constexpr int kLdsTok = kStages * 2 * kStageBytes;
 constexpr int kGemmLds = kLdsTok + kGT * 4 + 64;
 // D[16x16] += A[16 x 32] . B[16 x 32]^T (v_mfma_f32_16x16x32_bf16): lane
@@ -65,6 +68,7 @@ __global__ __launch_bounds__(kGThreads) void k_linear_lora(
     const float* __restrict__ scalings, int mtiles, int ntiles) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int* tok = (int*)(lds + kLdsTok);
+  int* unfit = tok + kGT;
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const int w = wave_id();
@@ -100,6 +104,7 @@ __global__ __launch_bounds__(kGThreads) void k_linear_lora(
     const int p = m0 + tid;
     tok[tid] = p >= T ? -1 : token_order ? min(max(token_order[p], 0), T - 1) : p;
   }
+  if (tid == 0) *unfit = 0;
   __syncthreads();
 
   const rsrc_t x_r = make_rsrc(x_, (uint32_t)T * (uint32_t)in * 2u);
@@ -223,10 +228,16 @@ __global__ __launch_bounds__(kGThreads) void k_linear_lora(
               hbits[e] = to_bf16_bits(v);
               lbits[e] = to_bf16_bits(v - __uint_as_float(hbits[e] << 16));
             }
-            const u32x4 hp = u32x4{hbits[0] | (hbits[1] << 16), hbits[2] | (hbits[3] << 16),
-                                   hbits[4] | (hbits[5] << 16), hbits[6] | (hbits[7] << 16)};
-            const u32x4 lp = u32x4{lbits[0] | (lbits[1] << 16), lbits[2] | (lbits[3] << 16),
-                                   lbits[4] | (lbits[5] << 16), lbits[6] | (lbits[7] << 16)};
+            u32x4 hp = u32x4{hbits[0] | (hbits[1] << 16), hbits[2] | (hbits[3] << 16),
+                             hbits[4] | (hbits[5] << 16), hbits[6] | (hbits[7] << 16)};
+            u32x4 lp = u32x4{lbits[0] | (lbits[1] << 16), lbits[2] | (lbits[3] << 16),
+                             lbits[4] | (lbits[5] << 16), lbits[6] | (lbits[7] << 16)};
+            if (not_finite(hp)) {
+              const u32x4 keep = finite_halves(hp);
+              hp &= keep;
+              lp &= keep;
+              *unfit = 1;
+            }
             *(u32x4*)(hb + swz4(row, q)) = hp;
             *(u32x4*)(hl + swz4(row, q)) = lp;
           }
@@ -248,6 +259,10 @@ __global__ __launch_bounds__(kGThreads) void k_linear_lora(
                   if (e < 2) bv.x &= keep; else if (e < 4) bv.y &= keep;
                   else if (e < 6) bv.z &= keep; else bv.w &= keep;
                 }
+              if (not_finite(bv)) {
+                bv &= finite_halves(bv);
+                *unfit = 1;
+              }
             }
             *(u32x4*)(bb + swz4(row, q)) = bv;
           }
@@ -279,6 +294,31 @@ __global__ __launch_bounds__(kGThreads) void k_linear_lora(
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+  if (__builtin_expect(h != nullptr && *unfit != 0, 0)) {   // seldom: 4 columns of a token at a time
+    int si = 0;
+    while (si + 1 < st.n && st.off[si + 1] <= n0) ++si;
+#pragma unroll 1
+    for (int u = 0; u < 32; ++u) {
+      const int row = wm * 128 + u % 8 * 16 + m, p = m0 + row;
+      const int col = n0 + wn * 64 + u / 8 * 16 + 4 * g;
+      f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (p < T && col < out) {
+        const int s = slot_of_position(indptr, slots, p);
+        int seg0 = 0, n = 0;
+        if (s < slots) segment_of(indptr, s, T, seg0, n);
+        if (p >= seg0 && p < seg0 + n) {
+          const float* ht = h + ((int64_t)tok[row] * st.n + si) * R;
+          const uint16_t* bt = (const uint16_t*)b_ + ((int64_t)s * out + col) * R;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            z[q] = unfit_sum(ht, bt + (int64_t)q * R, clamp_rank(ranks[s], R), scalings[s]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        if (u == q) acc[q / 8][q % 8] += z;
+    }
+  }
   const rsrc_t y_r = make_rsrc(y_, (uint32_t)T * (uint32_t)out * 2u);
 #pragma unroll
   for (int bq = 0; bq < 8; ++bq) {
