@@ -162,13 +162,19 @@ __device__ __forceinline__ u32x4 finite_halves(u32x4 v) {
            ((v[k] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
   return m;
 }
-// The sum of the products that one of them is a factor of, over r ranks.
+// The sum of the products that one of them is a factor of, over r ranks, 8 at a
+// time (R is a multiple of 8 in bf16, rows start at 16 bytes).
 __device__ __forceinline__ float unfit_sum(const float* h, const uint16_t* b, int r, float scale) {
   float z = 0.0f;
 #pragma unroll 1
-  for (int k = 0; k < r; ++k) {
-    const float x = h[k] * scale, y = __uint_as_float((uint32_t)b[k] << 16);
-    if (!fits_bf16(x) || !fits_bf16(y)) z = fmaf(x, y, z);
+  for (int k0 = 0; k0 < r; k0 += 8) {
+    const u32x4 bv = *(const u32x4*)(b + k0);
+    const f32x4 hv[2] = {*(const f32x4*)(h + k0), *(const f32x4*)(h + k0 + 4)};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = hv[k / 4][k % 4] * scale, y = k & 1 ? bf16hi(bv[k / 2]) : bf16lo(bv[k / 2]);
+      if (k0 + k < r && (!fits_bf16(x) || !fits_bf16(y))) z = fmaf(x, y, z);
+    }
   }
   return z;
 }
