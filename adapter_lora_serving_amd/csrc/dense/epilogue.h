@@ -208,7 +208,7 @@ constexpr int vm_lds_le(int n) { return vmcnt_le(n) & ~(15 << 8); }
 
 // h of a token, scaled, as `TERMS` bf16 parts whose sum it is: the high part
 // and what that leaves, so that the delta has h in 16 bits of fraction (2
-// terms, for a bf16 result) or all of its 24 (3 terms). Values that do not fit
+// terms) or all of its 24 (3 terms). Values that do not fit
 // bf16 show in the high part and are not for the matrix unit.
 template <int TERMS>
 __device__ __forceinline__ void split_bf16(const float* v, u32x4* out) {

@@ -627,8 +627,9 @@ void k_linear_tile(LinearArgs a, int sld, int mtiles, int ntiles) {
     // take 2 us, so the loads of kTurns turns are on their way at a time.
     bool unfit = false;   // values that are not for the matrix unit: see add_unfit
     if (e.h) {
-      // h in 24 bits of fraction where y is float32 or goes on to its codes, else in 16
-      constexpr int TERMS = GATED && !OP::kWide ? 2 : 3;
+      // h in all its 24 bits of fraction; in 16 in gated products by the scaled
+      // instruction, which has no codes to follow and loses 2^-16 itself
+      constexpr int TERMS = GATED && OP::kMX && !OP::kWide ? 2 : 3;
       constexpr int PARTS = GATED ? 2 : 1;   // gates and ups have slices of their own
       constexpr int kTurns = TM * TN > 4 ? 2 : 4;   // as the registers allow
       const int SR = e.slices * e.R, out = PARTS * e.N;

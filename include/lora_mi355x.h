@@ -679,8 +679,9 @@ lora_status lora_epilogue_linear(int operands, const void* x, const uint8_t* x_s
  * delta + bias and W [2 N, K], the gates' rows first; both projections, the
  * activation and the product are one kernel. With codes not NULL, codes and
  * scales receive MXFP8 of the rounded rows (N a multiple of 32), whose MXFP8
- * products are then summed as for a float32 y. Operands and e as above, without
- * a residual; W's scales are below 2 GiB.
+ * products are then summed as for a float32 y. MXFP8 operands without codes take
+ * h in 16 bits of fraction from 33 rows on. Operands and e as above, without a
+ * residual; W's scales are below 2 GiB.
  */
 lora_status lora_gated_linear(int operands, const void* x, const uint8_t* x_scales, int64_t T,
                               const void* w, const uint8_t* w_scales, int64_t N, int64_t K,

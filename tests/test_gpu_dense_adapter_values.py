@@ -1,12 +1,13 @@
-"""What an adapter's own rows get from the dense layer's products: h and B at the ends
-of their types as the formula has them."""
+"""What an adapter's own rows get from the dense layer's products: h in all the bits
+that the result shows, and h and B at the ends of their types as the formula has
+them."""
 import numpy as np
 import pytest
 
 import adapter_lora_serving_amd as L
 from gpu_util import f64, torch
 from oracle import dense_oracle as D
-from test_gpu_dense import DEV, EPS, bf16, gpu, near
+from test_gpu_dense import DEV, EPS, bf16, codes_of, gpu, near
 
 pytestmark = pytest.mark.gpu
 
@@ -81,5 +82,26 @@ def test_h_at_the_end_of_float32(T):
     two = d._replace(out_slices=(N // 2, N // 2), h=gpu(np.concatenate([h, h], 1)))
     rows = f64(L.gated_linear(x, w, activation=None, delta=two))
     g, u = ref[:, : N // 2], ref[:, N // 2:]
-    # two parts leave 2^-17 of h
+    # two parts of h leave 2^-17 of it, three nothing
     near(rows, g * u, 2.1 * (2.0**-17 + 8 * EPS) * np.abs(g * u), "rows", t.bfloat16)
+
+
+@pytest.mark.parametrize("T", [4, 70, 300, 2000])
+def test_codes_show_all_bits_of_h(T):
+    """Rows that go on to their codes take h in 24 bits, also of bf16 operands: what is left
+    of 1 + 2^-10 + 2^-20 by a base product of -1 and a bias of -2^-10 is 2^-20."""
+    t = torch()
+    N, K, R = 4064, 32, 8
+    h = np.full((T, 2 * R), 1.0 + 2.0**-10 + 2.0**-20, np.float32)
+    b = np.zeros((1, 2 * N, R), np.float32)
+    b[0, :N, 3] = 1.0
+    d, _ = delta_of(h, b, np.ones(1, np.float32), (N, N))
+    x, w = t.zeros(T, K, device=DEV), t.zeros(2 * N, K, device=DEV)
+    x[:, 0], w[:N, 0], w[N:, 0] = 1.0, -1.0, 1.0
+    bias = t.zeros(2 * N, device=DEV)
+    bias[:N] = -2.0**-10
+    x, w = x.bfloat16(), w.bfloat16()
+    for xo, wo in ((x, w), (L.quantize_mxfp8(x), L.quantize_mxfp8(w))):
+        rows, q = L.gated_linear_quantize_mxfp8(xo, wo, bias=bias, activation=None, delta=d)
+        assert (rows == 2.0**-20).all()
+        assert (L.dequantize_mxfp8(q) == 2.0**-20).all()
