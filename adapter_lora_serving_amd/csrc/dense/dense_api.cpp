@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "dense.h"
+#include "linear_choice.h"
 
 namespace {
 
@@ -193,6 +194,25 @@ lora_status lora_gated_linear(int operands, const void* x, const uint8_t* x_scal
                               void* stream) {
   return linear_impl(operands, true, x, x_scales, T, w, w_scales, N, K, e, LORA_BF16, rows, codes,
                      scales, stream);
+}
+
+// Not part of the C ABI: the kernel of a product on `units` compute units, as
+// rows, cols and each of LinearChoice, for tests that have to reach all of them.
+void lora_test_linear_choice(int mx, int gated, int y_f32, int residual, int T, int N, int K, int units,
+                             int32_t* choice) {
+  lora::LinearArgs a = {};
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.y_f32 = y_f32;
+  a.residual = residual ? choice : nullptr;   // whether there is one counts
+  const lora::LinearChoice c = mx ? (gated ? lora::choose_linear<true, true>(a, units)
+                                           : lora::choose_linear<true, false>(a, units))
+                                  : (gated ? lora::choose_linear<false, true>(a, units)
+                                           : lora::choose_linear<false, false>(a, units));
+  choice[0] = c.rows;
+  choice[1] = c.cols;
+  choice[2] = c.each;
 }
 
 }  // extern "C"

@@ -374,66 +374,37 @@ hipError_t launch_thin_by_width(const LinearArgs& a, hipStream_t stream, int dev
   else return launch_thin<OP, GATED, XD, 1, XD == 4 ? 6 : 8, 2>(a, stream, dev);
 }
 
-// What a product in tiles of BM x BN takes, in quarters of the time of a stage
-// of a 64 x 64 tile that has its compute unit for itself (0.29 us in bf16, 0.36
-// in MXFP8): `stage` times the stages and what a tile's y and residual take, for
-// as many rounds as the units need, with EACH tiles a unit at a time.
-template <bool GATED, int BM, int BN, int EACH = 1>
-int64_t cost_of(const LinearArgs& a, int cus, int stages, int stage) {
-  const int64_t tiles = (int64_t)tiles_of(a.T, BM) * tiles_of(a.N, GATED ? BN / 2 : BN);
-  const int bytes = (a.y_f32 ? 4 : 2) * (a.residual ? 2 : 1);
-  return (tiles + EACH * cus - 1) / (EACH * cus) *
-         ((int64_t)stages * stage + EACH * BM * BN / (GATED ? 2 : 1) * bytes / 800);
-}
-
-// Larger tiles read each operand less often and have more products for every
-// barrier; smaller ones leave fewer compute units idle. Measured, us, 64 x 64 /
-// 64 x 128 / 128 x 128 / 256 x 128 / 256 x 256, MXFP8:
-//   256 x  6144, K  4096:  28.5 /  21.3 /  27.6 /       /  76.7
-//   512 x  6144, K  4096:  42.0 /  41.5 /  28.2 /  47.8 /
-//  1024 x  6144, K  4096:  76.2 /  60.5 /  53.4 /  49.2 /  76.5
-//   256 x  4096, K 14336:  45.2 /  61.6 /  79.0 /       / 224.9
-//  1024 x  4096, K 14336: 154.0 / 117.0 /  82.2 / 148.2 / 208.6
-// and of gated pairs of 14336 columns, K 4096, from 64 x 128 on:
-//   256 rows 80.5 / 55.0 / 51.4 / 75.8, 512 rows 135.7 / 98.8 / 87.5 / 69.9.
+// The kernel that linear_choice.h names.
 template <class OP, bool GATED>
 hipError_t launch_by_size(const LinearArgs& a, hipStream_t stream) {
   int dev = 0, cus = 0;
   const hipError_t e = dense_compute_units(&dev, &cus);
   if (e != hipSuccess) return e;
-  if (a.T <= 8) return launch_thin_by_width<OP, GATED, 1>(a, stream, dev);
-  if (a.T <= 16) return launch_thin_by_width<OP, GATED, 2>(a, stream, dev);
-  if (a.T <= 32) return launch_thin_by_width<OP, GATED, 4>(a, stream, dev);
-  // Up to 64 rows where that is one round of workgroups, all of whose x each of
-  // them reads: 64 x 4096, K 14336 31 us (tiles of 64 x 64: 46), 64 x 6144, K
-  // 4096 14.9 (17.0); gated pairs of 14336 columns 41 (tiles: 33).
-  if constexpr (!GATED) {
-    if (a.T <= 64 && tiles_of(a.N, 16) <= cus) return launch_thin<OP, GATED, 8, 1, 4, 3>(a, stream, dev);
-    if (a.T <= 64 && tiles_of(a.N, 32) <= cus) return launch_thin<OP, GATED, 8, 2, 5, 2>(a, stream, dev);
+  const LinearChoice c = choose_linear<OP::kMX, GATED>(a, cus);
+  if (c.each == 0) {
+    if (c.rows == 8) return launch_thin_by_width<OP, GATED, 1>(a, stream, dev);
+    if (c.rows == 16) return launch_thin_by_width<OP, GATED, 2>(a, stream, dev);
+    if (c.rows == 32) return launch_thin_by_width<OP, GATED, 4>(a, stream, dev);
+    if constexpr (!GATED) {
+      if (c.cols == 16) return launch_thin<OP, GATED, 8, 1, 4, 3>(a, stream, dev);
+      return launch_thin<OP, GATED, 8, 2, 5, 2>(a, stream, dev);
+    }
+    return hipErrorInvalidValue;   // not reached: gated ones have 32 rows at most
   }
-  const int stages = tiles_of(a.K * (OP::kMX ? 1 : 2), kRowB);
-  const int64_t c256 = cost_of<GATED, 256, 256>(a, cus, stages, 20);
-  // Between the two: 256 x 128 in MXFP8; in bf16 two workgroups of 128 x 128 a
-  // unit with two stages each instead of three (1024 x 6144, K 4096: 70 us, in 256
-  // x 128 80; MXFP8 76 and 49, for the room that scales take in LDS).
-  const int64_t c384 = OP::kMX ? cost_of<GATED, 256, 128>(a, cus, stages, 15)
-                               : cost_of<GATED, 128, 128, 2>(a, cus, stages, 14);
-  const int64_t c128 = cost_of<GATED, 128, 128>(a, cus, stages, 8);
-  const int64_t c192 = cost_of<GATED, 64, 128>(a, cus, stages, 6);
-  const int64_t c64 = GATED ? c192 + 1 : cost_of<GATED, 64, 64>(a, cus, stages, 4);
-  const int64_t least = std::min({c256, c384, c128, c192, c64});
   // Eight waves, two for each SIMD, one of which multiplies while the other
   // reads; four where the conversions of a float32 result take the registers of
   // eight, and where a wave would be left with one tile of gates (55 us for 60).
-  if (c256 == least) return launch_tile<OP, GATED, 256, 256, OP::kWide ? 2 : 4, 2, 2>(a, stream, dev, cus);
-  if (c128 == least) return launch_tile<OP, GATED, 128, 128, GATED ? 2 : 4, 2, 3>(a, stream, dev, cus);
-  if (c384 == least) {
-    if constexpr (OP::kMX) return launch_tile<OP, GATED, 256, 128, 4, 2, 2>(a, stream, dev, cus);
-    else return launch_tile<OP, GATED, 128, 128, 2, 2, 2>(a, stream, dev, cus);
+  if (c.rows == 256 && c.cols == 256)
+    return launch_tile<OP, GATED, 256, 256, OP::kWide ? 2 : 4, 2, 2>(a, stream, dev, cus);
+  if constexpr (OP::kMX) {
+    if (c.rows == 256) return launch_tile<OP, GATED, 256, 128, 4, 2, 2>(a, stream, dev, cus);
+  } else {
+    if (c.each == 2) return launch_tile<OP, GATED, 128, 128, 2, 2, 2>(a, stream, dev, cus);
   }
-  if (c192 == least) return launch_tile<OP, GATED, 64, 128, 2, GATED ? 2 : 4, 4>(a, stream, dev, cus);
+  if (c.rows == 128) return launch_tile<OP, GATED, 128, 128, GATED ? 2 : 4, 2, 3>(a, stream, dev, cus);
+  if (c.cols == 128) return launch_tile<OP, GATED, 64, 128, 2, GATED ? 2 : 4, 4>(a, stream, dev, cus);
   if constexpr (!GATED) return launch_tile<OP, GATED, 64, 64, 2, 2, 4>(a, stream, dev, cus);
-  return hipErrorInvalidValue;   // not reached: one of the costs is the least
+  return hipErrorInvalidValue;   // not reached: gated ones have 128 columns at least
 }
 
 }  // namespace lora

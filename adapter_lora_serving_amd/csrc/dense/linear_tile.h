@@ -23,6 +23,7 @@
 #include <atomic>
 #include <type_traits>
 #include "epilogue.h"
+#include "linear_choice.h"
 
 namespace lora {
 
@@ -40,8 +41,6 @@ inline hipError_t dense_compute_units(int* dev, int* n) {
 }
 
 namespace {
-
-constexpr int kRowB = 128;       // bytes of a row in one LDS stage: K of 64 (bf16) or 128
 
 // Operand forms: steps of a stage, 16-byte chunks a lane supplies per step.
 // bf16, K 16 a step: chunk 2 j + h. MXFP8, K 64 a step: a lane's 32 bytes are
@@ -96,10 +95,6 @@ __device__ __forceinline__ u32x4 wide8(const u32x4* o, uint32_t word) {
 __device__ __forceinline__ uint32_t keep_blocks(int b, int kb) {
   const int n = kb - b;
   return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-}
-
-__host__ __device__ __forceinline__ int tiles_of(int n, int tile) {
-  return (int)(((uint32_t)n + (uint32_t)tile - 1) / (uint32_t)tile);
 }
 
 // LDS of a tile kernel: NST stages of both operands' rows, and as many groups
