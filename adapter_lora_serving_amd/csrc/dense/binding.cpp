@@ -57,6 +57,23 @@ Operand operand(Call& c, PyObject* o, const char* name) {
   return r;
 }
 
+// The error of an argument of another kind goes, any other stays and is raised.
+void not_that() {
+  if (!PyErr_ExceptionMatches(PyExc_TypeError) && !PyErr_ExceptionMatches(PyExc_ValueError) &&
+      !PyErr_ExceptionMatches(PyExc_OverflowError))
+    throw python_error();
+  PyErr_Clear();
+}
+
+double number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    not_that();
+    refuse("%s must be a number", name);
+  }
+  return v;
+}
+
 // The epilogue's arguments, and what keeps their tensors alive over the call.
 struct Epilogue {
   lora_epilogue e = {};
@@ -76,8 +93,11 @@ void take_delta(Call& c, PyObject* d, int64_t T, int64_t out, Epilogue& p) {
   p.indptr = c.int32(PyTuple_GET_ITEM(addr, 1), "slot_indptr");
   p.ranks = c.int32(PyTuple_GET_ITEM(d, 3), "delta.ranks");
   p.scalings = c.tensor(PyTuple_GET_ITEM(d, 4), "delta.scalings");
-  PyObject* seq = PySequence_Fast(PyTuple_GET_ITEM(d, 5), "delta.out_slices must be a sequence");
-  if (!seq) throw python_error();
+  PyObject* seq = PySequence_Fast(PyTuple_GET_ITEM(d, 5), "");
+  if (!seq) {
+    not_that();
+    refuse("delta.out_slices must be a sequence");
+  }
   bool whole = true;
   for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(seq) && whole; ++i) {
     const int64_t w = PyLong_AsLongLong(PySequence_Fast_GET_ITEM(seq, i));
@@ -190,6 +210,7 @@ PyObject* gated(PyObject* const* a) {
 
 // (x, weight, residual, eps, offset, held, residual_out) -> (rows, residual_out, codes, scales)
 PyObject* norm(PyObject* const* a) {
+  const double eps = number(a[3], "eps"), offset = number(a[4], "weight_offset");
   Call c;
   const at::Tensor x = c.tensor(a[0], "x"), weight = c.tensor(a[1], "weight");
   if (x.dim() != 2) refuse("x must be [T, width]");
@@ -201,8 +222,6 @@ PyObject* norm(PyObject* const* a) {
   if (residual) given(*residual, T, H, x.scalar_type(), "residual");
   if (out_in && !residual) refuse("residual_out goes with a residual");
   if (out_in) given(*out_in, T, H, x.scalar_type(), "residual_out");
-  const double eps = PyFloat_AsDouble(a[3]), offset = PyFloat_AsDouble(a[4]);
-  if (PyErr_Occurred()) throw python_error();
   const bool held = a[5] == Py_True;
   const int64_t ld = held ? lora_mxfp8_scale_row_bytes(H) : 0;
   if (held && ld == 0) refuse("rows in MXFP8 must be a multiple of 32 wide, at most 2^20");
