@@ -162,3 +162,17 @@ def test_codes_of_two_threads(T, form):
     for th in threads:
         th.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx"])
+@pytest.mark.parametrize("T", [5, 30, 130])
+@pytest.mark.parametrize("N,slices", [(100, (96, 104)), (36, (72,)), (44, (8, 72, 8)), (96, (40, 112, 40))])
+def test_slices_across_gates_and_ups(N, slices, T, form):
+    """A slice may hold the last gates and the first ups; N may end within 8 columns."""
+    c = Case(T, 2 * N, 160, form, slices, T + N)
+    g, u = c.z[:, :N], c.z[:, N:]
+    dz = c.exact if form == "bf16" else c.scaled
+    a = silu(g)
+    da, du = silu_bound(g, dz[:, :N], a), dz[:, N:]
+    bound = da * (u.abs() + du) + a.abs() * du + 2 * EPS * (a * u).abs()
+    near(L.gated_linear(c.x, c.w, bias=c.bias, delta=c.delta), a * u, bound)
