@@ -179,9 +179,9 @@ __device__ __forceinline__ void wide_step(const u32x4 (*wo)[2], const u32x4 (*xo
 //
 // What bounds it, 256 x 256: a stage's products, 1.06 us at the clock that the
 // power leaves, and its 64 KB on their way into LDS beside them. 8192 x 4096, K
-// 14336: bf16 731 us (1.32 PFLOP/s; 68 % of the matrix unit's cycles; 627
-// without transfers), MXFP8 409 us (2.35 PFLOP/s; 347), MXFP8 by way of bf16
-// 713 us. A tile's way out takes 11 to 15 us of about 120, its delta over one or
+// 14336: bf16 731 us (1.32 PFLOP/s; about 70 % of the matrix unit's cycles; 627
+// without transfers), MXFP8 409 to 460 us (2.1 to 2.35 PFLOP/s; half of those
+// cycles; 347), MXFP8 by way of bf16 713 us. A tile's way out takes 11 to 15 us of about 120, its delta over one or
 // two slots of 64 ranks 15. Smaller tiles: the time of a stage, 0.3 to 0.6 us
 // for what its products and bytes would take half of.
 template <class OP, bool GATED, int BM, int BN, int WM, int WN, int NST>

@@ -595,7 +595,8 @@ enum { LORA_ACT_NONE = 0, LORA_ACT_RELU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TA
  * residual_out receives s (NULL exactly where residual is; it may be residual
  * itself, or x). weight is [width] of dtype. With codes not NULL, codes and
  * scales receive MXFP8 of the rounded rows, the same bytes as quantising
- * them. Sums are float32: a row whose squares pass it gives zeros, and a row
+ * them. Sums are float32: a row whose squares pass it gives zeros (with eps 0
+ * infinities, where they vanish in it), and a row
  * that holds a NaN or an infinity gives NaN where the formula does. width is
  * a multiple of 8, with codes of 32. rows may be x; otherwise outputs overlap
  * no other argument.
@@ -627,7 +628,9 @@ lora_status lora_dequantize_mxfp8(int dtype, const uint8_t* codes, const uint8_t
  * shrink's [T, num_slices * R] for the adapters' b [slots, out, R] (bf16),
  * with the addressing, ranks and scalings of lora_expand and out_slices (host)
  * the num_slices widths, whose sum is out. Columns of h and b past a slot's
- * rank do not count. out is the number of W's rows: N, or 2 N of a gated
+ * rank do not count, and a token's delta depends on its own slot and h alone:
+ * an infinity or a NaN of another slot, or of another slice's h, does not reach
+ * it. out is the number of W's rows: N, or 2 N of a gated
  * product.
  */
 typedef struct lora_epilogue {
@@ -665,9 +668,10 @@ typedef struct lora_epilogue {
  * lost. A float32 y has exact products and float32 sums, of values in bf16's
  * range: an MXFP8 value of 2^128 or more is infinite there, and one below 2^-126
  * may count as 0. Everything after them is float32 and is rounded once to dtype
- * (of y and residual). silu(z) = z / (1 + exp(-z)); gelu(z) = z / 2 (1 + erf(z / sqrt 2)); gelu_tanh its form with tanh(sqrt(2 /
- * pi) (z + 0.044715 z^3)). e may be NULL (none of it). With a delta x and
- * h are below 2 GiB (else LORA_ERR_UNSUPPORTED). T = 0 does nothing.
+ * (of y and residual). silu(z) = z / (1 + exp(-z)); gelu(z) = z / 2 (1 + erf(z
+ * / sqrt 2)); gelu_tanh its form with tanh(sqrt(2 / pi) (z + 0.044715 z^3)).
+ * e may be NULL (none of it). With a delta x and h are below 2 GiB (else
+ * LORA_ERR_UNSUPPORTED). T = 0 does nothing.
  * y overlaps no other argument but residual.
  */
 lora_status lora_epilogue_linear(int operands, const void* x, const uint8_t* x_scales, int64_t T,
