@@ -181,9 +181,10 @@ __device__ __forceinline__ void wide_step(const u32x4 (*wo)[2], const u32x4 (*xo
 // power leaves, and its 64 KB on their way into LDS beside them. 8192 x 4096, K
 // 14336: bf16 731 us (1.32 PFLOP/s; about 70 % of the matrix unit's cycles; 627
 // without transfers), MXFP8 409 to 460 us (2.1 to 2.35 PFLOP/s; half of those
-// cycles; 347), MXFP8 by way of bf16 713 us. A tile's way out takes 11 to 15 us of about 120, its delta over one or
-// two slots of 64 ranks 15. Smaller tiles: the time of a stage, 0.3 to 0.6 us
-// for what its products and bytes would take half of.
+// cycles; 347 without transfers), MXFP8 by way of bf16 713 us. A tile's way out
+// takes 11 to 15 us of about 120, its delta over one or two slots of 64 ranks 15.
+// Smaller tiles: the time of a stage, 0.3 to 0.6 us for what its products and
+// bytes would take half of.
 template <class OP, bool GATED, int BM, int BN, int WM, int WN, int NST>
 __global__ __launch_bounds__(64 * WM * WN, (Lds<OP, BM, BN, WM * WN, NST>::kOccupancy * WM * WN + 3) / 4)
 void k_linear_tile(LinearArgs a, int sld, int mtiles, int ntiles) {
@@ -620,7 +621,9 @@ void k_linear_tile(LinearArgs a, int sld, int mtiles, int ntiles) {
     // and 16 ranks at a time: scaling * h as bf16 parts (other rows 0) against
     // the slot's B, on the accumulators. A turn is a few products and its loads
     // take 2 us, so the loads of kTurns turns are on their way at a time.
-    bool unfit = false;   // values that are not for the matrix unit: see add_unfit
+    // Looking for values that are not for it, see add_unfit, takes 0 to 1 % of a
+    // product; having one 4 to 6 times the product's time at 8192 rows.
+    bool unfit = false;
     if (e.h) {
       // h in all its 24 bits of fraction; in 16 in gated products by the scaled
       // instruction, which has no codes to follow and loses 2^-16 itself

@@ -113,3 +113,56 @@ def test_gated_keeps_them_where_they_belong(T, N, form, held, poison):
         hit = hit[:, :N] | hit[:, N:]
         assert t.equal(y[~hit], clean[~hit]), (part, int((y[~hit] != clean[~hit]).sum()))
         assert not t.isfinite(y[hit]).any()
+
+
+def test_malformed_addressing_with_them():
+    """Positions, bounds and ranks out of range beside values that are not finite: some y, and
+    no access outside."""
+    t = torch()
+    rng = np.random.default_rng(3)
+    T, N, slots = 130, 128, 4
+    x, w = bf16(rng, T, 64)[1], bf16(rng, N, 64)[1]
+    b = bf16(rng, slots, N, R)[1]
+    b[1:] = float("nan")
+    h = t.full((T, R), float("inf"), device=DEV)
+    big = 2**31 - 1
+    for order, indptr, ranks in ((np.full(T, big), [0, 20, 40, 60, T], [24, 99, -3, big]),
+                                 (np.full(T, -5), [0, 20, 40, 60, T], [24] * 4),
+                                 (np.arange(T), [50, 20, big, -7, T], [24] * 4),
+                                 (np.arange(T), [-big, 3, 200, T, big], [24] * 4)):
+        i32 = lambda v: gpu(np.asarray(v).astype(np.int32))   # noqa: E731
+        d = L.Delta(h, b, L.Addressing(i32(order), i32(indptr)), i32(ranks), t.ones(slots, device=DEV), (N,))
+        L.epilogue_linear(x, w, delta=d, activation="relu")
+        L.gated_linear(x, w, delta=d)
+    t.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T", [20, 150])
+def test_replayed_as_a_graph(T):
+    """A captured call whose adapters become bad, and good again, between its replays."""
+    t = torch()
+    rng = np.random.default_rng(T)
+    x, w = bf16(rng, T, 64)[1], bf16(rng, 192, 64)[1]
+    a = Adapters(rng, T, (96, 96), 5)
+    good, bad = a.delta().b.clone(), a.delta("b_inf", 1, 100).b
+    d = a.delta()._replace(b=good.clone())
+
+    def step():
+        return L.epilogue_linear(x, w, delta=d), L.gated_linear_quantize_mxfp8(x, w, delta=d)[0]
+
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        step()
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g, stream=side):
+            out = step()
+    t.cuda.synchronize()
+    for b in (good, bad, good, bad, good):
+        d.b.copy_(b)
+        eager = step()
+        t.cuda.synchronize()
+        g.replay()
+        t.cuda.synchronize()
+        for e, o in zip(eager, out):
+            assert t.equal(e.view(t.int16), o.view(t.int16))
